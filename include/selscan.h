@@ -2,7 +2,8 @@
  * selscan.h -- C ABI of libselscan, the selective scan (S6) on NVIDIA B200
  * (sm_100a): the forward pass over a sequence (diagonal A, and scalar A in
  * the chunked matrix form on the tensor cores), the one-token decode step of
- * both, and the backward pass of the diagonal form.
+ * both, the backward passes, the scan of packed prompts through a cache of
+ * states, and the short causal convolution in front of the scan.
  *
  * What is computed (diagonal A).  For every batch b, channel d and token t,
  * following "03 -- Modelos de espacio de estados: RWKV, S4, Mamba y el
@@ -38,8 +39,9 @@
  *     entry points take per-token tensors with any strides; see there.)
  *   - Validation errors are returned synchronously and nothing is launched.
  *     A failed launch returns SELSCAN_ERR_CUDA.  A device-side wait that ran
- *     out of its iteration limit is recorded on the device and reported by
- *     the next selscan_check().
+ *     out of its iteration limit, and an index read on the device (a slot, a
+ *     sequence start) that is refused there, are recorded on the device and
+ *     reported by the next selscan_check().
  *   - There is no CPU fallback: every step runs in this library's kernels.
  */
 #ifndef SELSCAN_H
@@ -69,10 +71,12 @@ typedef enum {
     SELSCAN_ERR_ALIGN = 5,       /* pointer / row stride not 16B aligned */
     SELSCAN_ERR_UNSUPPORTED = 6, /* valid but not built (e.g. N != 16)   */
     SELSCAN_ERR_CUDA = 7,        /* a CUDA runtime call failed           */
-    SELSCAN_ERR_TIMEOUT = 8      /* a device-side wait gave up           */
+    SELSCAN_ERR_TIMEOUT = 8,     /* a device-side wait gave up           */
+    SELSCAN_ERR_INDEX = 9        /* a device-side index was refused      */
 } selscan_status;
 
-typedef enum { SELSCAN_F32 = 0, SELSCAN_BF16 = 1 } selscan_dtype;
+/* SELSCAN_I32: index arrays (slots, sequence starts, tokens seen) only. */
+typedef enum { SELSCAN_F32 = 0, SELSCAN_BF16 = 1, SELSCAN_I32 = 2 } selscan_dtype;
 
 typedef struct {
     void *data;        /* device pointer (NULL allowed only where noted) */
@@ -275,6 +279,163 @@ SELSCAN_API selscan_status selscan_step_scalarA(selscan_tensor *state, const sel
                                     int64_t headdim, selscan_tensor *y, cudaStream_t stream);
 
 /*
+ * selscan_step_slots, selscan_step_scalarA_slots -- the decode steps above
+ * through a cache of states: state is (count, D, N) or (count, H, P, N), and
+ * row b of the batch updates state[slots[b]].
+ *
+ *   slots      (batch)        I32, contiguous, on the device.  A negative slot
+ *                             marks a padding row: it is skipped, its row of y
+ *                             is left as it was.
+ *
+ * A slot past the cache's end, or one that an earlier row of the batch has
+ * (two rows would race on one state), is refused on the device: the row is
+ * skipped and selscan_check() returns SELSCAN_ERR_INDEX.  Everything else as
+ * in selscan_step and selscan_step_scalarA.
+ */
+SELSCAN_API selscan_status selscan_step_slots(
+    selscan_tensor *state, const selscan_tensor *slots, const selscan_tensor *u,
+    const selscan_tensor *delta, const selscan_tensor *delta_bias, int delta_softplus,
+    const selscan_tensor *A, const selscan_tensor *B, const selscan_tensor *C,
+    const selscan_tensor *D, const selscan_tensor *z, selscan_tensor *y, cudaStream_t stream);
+
+SELSCAN_API selscan_status selscan_step_scalarA_slots(
+    selscan_tensor *state, const selscan_tensor *slots, const selscan_tensor *x,
+    const selscan_tensor *dt, const selscan_tensor *dt_bias, int dt_softplus,
+    const selscan_tensor *A, const selscan_tensor *B, const selscan_tensor *C,
+    const selscan_tensor *D, const selscan_tensor *z, int64_t headdim, selscan_tensor *y,
+    cudaStream_t stream);
+
+/*
+ * selscan_fwd_packed -- the diagonal-A scan over packed prompts of unequal
+ * length, through a cache of states (prefill of a serving loop: whole prompts,
+ * chunks of prompts and single tokens in one call).  Token-major: row t holds
+ * one token.  Sequence i owns rows [start[i], start[i+1]) and state
+ * state[slots[i]], which holds the state after its last token when the call
+ * is done.
+ *
+ *   state      (count, D, N)  F32, contiguous, 16-byte aligned; read and
+ *                             overwritten at the sequences' slots only
+ *   u, delta, z (tokens, D)   F32 or BF16 (same); channel stride 1, any row
+ *                             stride; z may be NULL (no gate)
+ *   delta_bias, D (D)         F32; may be NULL
+ *   A          (D, N)         F32, contiguous, 16-byte aligned
+ *   B, C       (tokens, N)    same dtype as u; stride 1, any row stride
+ *   start      (seqs + 1)     I32, contiguous, on the device, non-decreasing,
+ *                             0 <= start[i] <= tokens
+ *   slots      (seqs)         I32, contiguous, on the device
+ *   seen       (seqs)         I32, contiguous, on the device: tokens already
+ *                             in the state; 0 starts from the zero state.
+ *                             NULL: every sequence continues its state.
+ *   y          (tokens, D)    like u; written; must not overlap an input
+ *
+ * A sequence may be empty (its state is kept, or zeroed where seen is 0).  A
+ * negative slot marks a padding sequence: it is skipped, its rows of y are
+ * left as they were, as are rows that belong to no sequence.  A sequence
+ * whose rows leave the buffer, whose slot is past the cache's end, or whose
+ * slot an earlier sequence has, is refused on the device: it is skipped and
+ * selscan_check() returns SELSCAN_ERR_INDEX.  (With starts that are not
+ * non-decreasing, rows may be written more than once or not at all.)
+ *
+ * N must be 16; at most 65535 sequences.  Arithmetic as in selscan_fwd.
+ * Sequences longer than a segment (a length chosen from the number of rows
+ * and channels) are scanned in two passes, with the segments' end states in
+ * stream-ordered scratch.
+ */
+SELSCAN_API selscan_status selscan_fwd_packed(
+    selscan_tensor *state, const selscan_tensor *u, const selscan_tensor *delta,
+    const selscan_tensor *delta_bias, int delta_softplus, const selscan_tensor *A,
+    const selscan_tensor *B, const selscan_tensor *C, const selscan_tensor *D,
+    const selscan_tensor *z, const selscan_tensor *start, const selscan_tensor *slots,
+    const selscan_tensor *seen, selscan_tensor *y, cudaStream_t stream);
+
+/*
+ * selscan_conv -- the short causal convolution that a layer applies to the
+ * scan's input, channel by channel:
+ *
+ *   v[b,d,t] = bias[d] + sum_{k<W} weight[d,k] x[b,d,t-(W-1)+k]
+ *   y[b,d,t] = v sigmoid(v)      (SiLU optional; without it y = v)
+ *
+ * with x at t < 0 taken from h0 (zero if NULL).
+ *
+ *   x, y       (batch, D, L)   F32 or BF16 (same); any strides.  Fast where
+ *                              the time or the channel stride is 1 and rows
+ *                              are 16-byte aligned; x and y may differ in
+ *                              that (a token-major projection filtered into
+ *                              the channels-first rows that the scan takes).
+ *   weight     (D, W)          F32, contiguous; W = 2, 3 or 4
+ *   bias       (D)             F32; may be NULL
+ *   h0         (batch, D, W-1) like x, contiguous; may be NULL: the W-1
+ *                              inputs before x
+ *   last_state (batch, D, W-1) like x, contiguous; may be NULL; written: the
+ *                              last W-1 inputs (h0's where L < W-1); may be
+ *                              the same buffer as h0
+ * y must not overlap x.  Sums are fp32.
+ */
+SELSCAN_API selscan_status selscan_conv(const selscan_tensor *x, const selscan_tensor *weight,
+                                        const selscan_tensor *bias, int silu,
+                                        const selscan_tensor *h0, selscan_tensor *y,
+                                        selscan_tensor *last_state, cudaStream_t stream);
+
+/*
+ * selscan_conv_bwd -- gradients of selscan_conv for the loss
+ *     sum(dy * y) + sum(dlast * last_state).
+ * With g = dy * silu'(v) (v recomputed; g = dy without SiLU) and e = [h0 | x]:
+ *   de[i] = sum_k weight[k] g[i-k] (+ dlast on the last W-1 of e),
+ *   dx and dh0 its two parts,  dweight[k] = sum g[t] e[t+k],  dbias = sum g.
+ *
+ *   x, weight, bias, silu, h0      as in selscan_conv
+ *   dy         (batch, D, L)       like x, any strides
+ *   dlast      (batch, D, W-1)     like x, contiguous; may be NULL (zero)
+ * Outputs (all overwritten):
+ *   dx         (batch, D, L)       like x, any strides (fastest in x's layout);
+ *                                  must not overlap x or dy
+ *   dweight    (D, W)              F32, contiguous
+ *   dbias      (D)                 F32; may be NULL (not computed)
+ *   dh0        (batch, D, W-1)     like x, contiguous; may be NULL (not
+ *                                  computed); must not overlap dlast
+ * The sums over tokens and batch rows are made in a fixed order (stream-
+ * ordered scratch, no atomics): the same inputs give the same bits.
+ */
+SELSCAN_API selscan_status selscan_conv_bwd(const selscan_tensor *x,
+                                            const selscan_tensor *weight,
+                                            const selscan_tensor *bias, int silu,
+                                            const selscan_tensor *h0, const selscan_tensor *dy,
+                                            const selscan_tensor *dlast, selscan_tensor *dx,
+                                            selscan_tensor *dweight, selscan_tensor *dbias,
+                                            selscan_tensor *dh0, cudaStream_t stream);
+
+/*
+ * selscan_conv_step -- one token of selscan_conv per row, state in place: row
+ * b filters [state | x[b]] and the state moves on by one input.
+ *
+ *   state      (count, D, W-1) like x, contiguous: row b's at slots[b], or at
+ *                              b where slots is NULL (count = batch)
+ *   slots      (batch)         I32, as in selscan_step_slots; may be NULL
+ *   x, y       (batch, D)      F32 or BF16 (same); any strides; y may be x
+ *   weight, bias, silu         as in selscan_conv
+ */
+SELSCAN_API selscan_status selscan_conv_step(selscan_tensor *state, const selscan_tensor *slots,
+                                             const selscan_tensor *x,
+                                             const selscan_tensor *weight,
+                                             const selscan_tensor *bias, int silu,
+                                             selscan_tensor *y, cudaStream_t stream);
+
+/*
+ * selscan_conv_packed -- selscan_conv over packed prompts of unequal length
+ * through a cache of states; x and y are (tokens, D), channel stride 1, any
+ * row stride; y must not overlap x; state (count, D, W-1) like x, contiguous;
+ * start, slots, seen, empty and padding sequences and refusals as in
+ * selscan_fwd_packed.
+ */
+SELSCAN_API selscan_status selscan_conv_packed(selscan_tensor *state, const selscan_tensor *x,
+                                               const selscan_tensor *weight,
+                                               const selscan_tensor *bias, int silu,
+                                               const selscan_tensor *start,
+                                               const selscan_tensor *slots,
+                                               const selscan_tensor *seen, selscan_tensor *y,
+                                               cudaStream_t stream);
+
+/*
  * selscan_bwd -- gradients of selscan_fwd_h0 (diagonal A) for the loss
  *     sum(dy * y) + sum(dlast * last_state)
  * (training differentiates the recurrence of the forward pass; "03 --
@@ -362,7 +523,8 @@ SELSCAN_API selscan_status selscan_bwd_scalarA(
 /*
  * selscan_check -- synchronise `stream` and report device-side errors that
  * earlier calls recorded (a bounded wait that gave up returns
- * SELSCAN_ERR_TIMEOUT; the record is then cleared).  Returns
+ * SELSCAN_ERR_TIMEOUT, otherwise a refused slot or sequence returns
+ * SELSCAN_ERR_INDEX; the record is then cleared).  Returns
  * SELSCAN_ERR_CUDA if the synchronisation itself failed.
  */
 SELSCAN_API selscan_status selscan_check(cudaStream_t stream);
@@ -380,8 +542,12 @@ SELSCAN_API int selscan_version(void);
  * sequences); selscan_bwd launches two (three with time segments: the
  * segment aggregates, the gradient walk, the sum of the dB / dC partial
  * copies); selscan_bwd_scalarA launches three (chunk states, the chunk
- * walk, the sum of the dB / dC copies); the other entry points launch one.  Benchmarks read it around
- * a timed region to report how many of the library's kernels ran in it.
+ * walk, the sum of the dB / dC copies); selscan_conv_bwd launches two (the
+ * gradients, the sum of the runs' weight gradients); selscan_fwd_packed one,
+ * or three where a sequence may be longer than a segment (segment ends, their
+ * fold, the output pass); the other entry points launch one.  Benchmarks read
+ * it around a timed region to report how many of the library's kernels ran in
+ * it.
  */
 SELSCAN_API unsigned long long selscan_launch_count(void);
 

@@ -1,4 +1,5 @@
-"""libselscan: selective-scan (S6) forward for NVIDIA B200 (sm_100a).
+"""libselscan: the selective scan (S6) and the short causal convolution in
+front of it, for NVIDIA B200 (sm_100a).
 
 This package is a thin ctypes binding over the C ABI in ``include/selscan.h``
 (built in-tree as ``libselscan.so`` by ``build.py``).  It only marshals
@@ -10,19 +11,23 @@ pointer, shape and strides.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libselscan.so")
 
 SELSCAN_F32 = 0
 SELSCAN_BF16 = 1
+SELSCAN_I32 = 2  # index arrays: slots, sequence starts, tokens seen
 
 STATUS = {
     0: "SELSCAN_OK", 1: "SELSCAN_ERR_NULL", 2: "SELSCAN_ERR_SHAPE",
     3: "SELSCAN_ERR_STRIDE", 4: "SELSCAN_ERR_DTYPE", 5: "SELSCAN_ERR_ALIGN",
     6: "SELSCAN_ERR_UNSUPPORTED", 7: "SELSCAN_ERR_CUDA", 8: "SELSCAN_ERR_TIMEOUT",
+    9: "SELSCAN_ERR_INDEX",
 }
 STATUS_CODE = {v: k for k, v in STATUS.items()}
 
@@ -30,7 +35,9 @@ STATUS_CODE = {v: k for k, v in STATUS.items()}
 EXPORTS = ("selscan_fwd", "selscan_fwd_h0", "selscan_fwd_scalarA", "selscan_fwd_scalarA_h0",
            "selscan_fwd_noalloc", "selscan_step", "selscan_step_scalarA", "selscan_check",
            "selscan_strerror", "selscan_version", "selscan_launch_count", "selscan_bwd",
-           "selscan_release_scratch")
+           "selscan_release_scratch", "selscan_step_slots", "selscan_step_scalarA_slots",
+           "selscan_fwd_packed", "selscan_conv", "selscan_conv_bwd", "selscan_conv_step",
+           "selscan_conv_packed")
 
 
 class SelscanError(RuntimeError):
@@ -95,6 +102,20 @@ def lib() -> ctypes.CDLL:
         L.selscan_bwd.restype = ctypes.c_int
         L.selscan_release_scratch.argtypes = []
         L.selscan_release_scratch.restype = ctypes.c_int
+        # descriptors of these come packed, as bytes (see _descs)
+        S, I, V = ctypes.c_char_p, ctypes.c_int, ctypes.c_void_p
+        L.selscan_step_slots.argtypes = [S] * 5 + [I] + [S] * 6 + [V]
+        L.selscan_step_scalarA_slots.argtypes = ([S] * 5 + [I] + [S] * 5 +
+                                                 [ctypes.c_int64, S, V])
+        L.selscan_fwd_packed.argtypes = [S] * 4 + [I] + [S] * 9 + [V]
+        L.selscan_conv.argtypes = [S] * 3 + [I] + [S] * 3 + [V]
+        L.selscan_conv_bwd.argtypes = [S] * 3 + [I] + [S] * 7 + [V]
+        L.selscan_conv_step.argtypes = [S] * 5 + [I, S, V]
+        L.selscan_conv_packed.argtypes = [S] * 4 + [I] + [S] * 4 + [V]
+        for f in (L.selscan_step_slots, L.selscan_step_scalarA_slots, L.selscan_fwd_packed,
+                  L.selscan_conv, L.selscan_conv_bwd, L.selscan_conv_step,
+                  L.selscan_conv_packed):
+            f.restype = ctypes.c_int
         L.selscan_debug_withhold_carry.argtypes = [ctypes.c_int]
         L.selscan_debug_withhold_carry.restype = None
         L.selscan_debug_diag_mode.argtypes = [ctypes.c_int]
@@ -160,6 +181,70 @@ def describe(t, dtype_code=None) -> SelscanTensor | None:
 
 def _ref(d):
     return None if d is None else ctypes.byref(d)
+
+
+# selscan_tensor as bytes: a decode step passes ten of them, and packing one
+# takes a fraction of the time of filling a ctypes structure field by field.
+_DESC = struct.Struct("Pii8q")
+_PAD = (0, 0, 0, 0)
+_CODES: dict = {}
+
+
+def _descs(*tensors):
+    """The device that all of the tensors (None: absent) are on, and their
+    packed selscan_tensor descriptors."""
+    if not _CODES:
+        import torch
+        _CODES.update({torch.float32: SELSCAN_F32, torch.bfloat16: SELSCAN_BF16,
+                       torch.int32: SELSCAN_I32})
+    dev, out = None, []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
+                raise ValueError("libselscan takes CUDA tensors only (got one on "
+                                 f"{t.device}); there is no CPU implementation")
+            if dev is not None:
+                raise ValueError(f"tensors on different devices (cuda:{dev} and cuda:{d})")
+            dev = d
+        shape = t.shape
+        n = len(shape)
+        if not 1 <= n <= 4:
+            raise ValueError(f"libselscan takes tensors of 1 to 4 dimensions (got {n})")
+        out.append(_DESC.pack(t.data_ptr(), _CODES.get(t.dtype, -1), n, *shape, *_PAD[n:],
+                              *t.stride(), *_PAD[n:]))
+    return dev, out
+
+
+def _launch(name, dev, stream, *args):
+    """Call an entry point with the tensors' device current, on ``stream`` (by
+    default that device's current stream)."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"{name}: the stream is on cuda:{stream.device_index}, the tensors "
+                         f"on cuda:{dev}")
+    f = getattr(lib(), name)
+    if torch.cuda.current_device() == dev:
+        rc = f(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, stream.cuda_stream)
+    if rc != 0:
+        raise SelscanError(rc, name)
+
+
+def _on(stream):
+    """Outputs are allocated on the stream that writes them, so that the
+    allocator does not hand out memory that another stream still uses."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    return torch.cuda.stream(stream)
 
 
 def _stream_handle(stream):
@@ -256,11 +341,21 @@ def selscan_fwd_scalarA(x, dt, A, B, C, headdim, D=None, z=None, dt_bias=None,
 
 
 def selscan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=None,
-                 delta_softplus=True, out=None, stream=None):
+                 delta_softplus=True, out=None, stream=None, slots=None):
     """One decode step of the diagonal-A scan; ``state`` (batch, D, N) fp32
     is updated in place.  u, delta, z: (batch, D) bf16 or fp32 (any strides);
-    B, C: (batch, N) or (batch, G, N).  Returns y (batch, D)."""
+    B, C: (batch, N) or (batch, G, N).  Returns y (batch, D).
+
+    With ``slots`` (batch,) int32 (selscan_step_slots) the state is a cache
+    (count, D, N) and row b updates state[slots[b]]; a negative slot marks a
+    padding row, whose row of ``out`` is left as it was."""
     import torch
+    if slots is not None:
+        with _on(stream):
+            y = out if out is not None else torch.empty(u.shape, dtype=u.dtype, device=u.device)
+        dev, d = _descs(state, slots, u, delta, delta_bias, A, B, C, D, z, y)
+        _launch("selscan_step_slots", dev, stream, *d[:5], int(bool(delta_softplus)), *d[5:])
+        return y
     y = out if out is not None else torch.empty(u.shape, dtype=u.dtype, device=u.device)
     d = [describe(t) for t in (state, u, delta, delta_bias, A, B, C, D, z, y)]
     rc = lib().selscan_step(_ref(d[0]), _ref(d[1]), _ref(d[2]), _ref(d[3]),
@@ -272,11 +367,21 @@ def selscan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=None,
 
 
 def selscan_step_scalarA(state, x, dt, A, B, C, headdim, D=None, z=None, dt_bias=None,
-                         dt_softplus=False, out=None, stream=None):
+                         dt_softplus=False, out=None, stream=None, slots=None):
     """One decode step of the scalar-A (Mamba-2) scan; ``state`` (batch, H,
     P, N) fp32 is updated in place.  x, z: (batch, H*P); dt: (batch, H)
-    fp32; B, C: (batch, N) or (batch, G, N).  Returns y (batch, H*P)."""
+    fp32; B, C: (batch, N) or (batch, G, N).  Returns y (batch, H*P).
+
+    With ``slots`` (batch,) int32 (selscan_step_scalarA_slots) the state is a
+    cache (count, H, P, N), as in selscan_step."""
     import torch
+    if slots is not None:
+        with _on(stream):
+            y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dev, d = _descs(state, slots, x, dt, dt_bias, A, B, C, D, z, y)
+        _launch("selscan_step_scalarA_slots", dev, stream, *d[:5], int(bool(dt_softplus)),
+                *d[5:10], int(headdim), d[10])
+        return y
     y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
     d = [describe(t) for t in (state, x, dt, dt_bias, A, B, C, D, z, y)]
     rc = lib().selscan_step_scalarA(_ref(d[0]), _ref(d[1]), _ref(d[2]), _ref(d[3]),
@@ -365,8 +470,103 @@ def selscan_bwd_scalarA(x, dt, A, B, C, headdim, dy, D=None, z=None, dt_bias=Non
     return out
 
 
+def selscan_fwd_packed(state, u, delta, A, B, C, start, slots, D=None, z=None,
+                       delta_bias=None, delta_softplus=True, seen=None, out=None, stream=None):
+    """The diagonal-A scan over packed prompts of unequal length, through a
+    cache of states.
+
+    u, delta, z: (tokens, D) bf16 or fp32, B, C: (tokens, N=16) like u (channel
+    stride 1, any row stride); sequence i owns rows start[i] to start[i+1] and
+    ``state[slots[i]]`` of the fp32 cache (count, D, N), which is updated in
+    place; start (seqs + 1,), slots (seqs,) and seen (seqs,) are int32 on the
+    device.  seen[i] == 0 starts sequence i from the zero state (seen None: all
+    continue their states).  A negative slot marks a padding sequence; its rows
+    of ``out``, and rows of no sequence, are left as they were.  Returns y
+    (tokens, D)."""
+    import torch
+    with _on(stream):
+        y = out if out is not None else torch.empty(u.shape, dtype=u.dtype, device=u.device)
+    dev, d = _descs(state, u, delta, delta_bias, A, B, C, D, z, start, slots, seen, y)
+    _launch("selscan_fwd_packed", dev, stream, *d[:4], int(bool(delta_softplus)), *d[4:])
+    return y
+
+
+def selscan_conv(x, weight, bias=None, silu=True, h0=None, out=None, last_state=None,
+                 return_last_state=True, stream=None):
+    """The short causal convolution in front of the scan (with SiLU unless
+    ``silu`` is false).
+
+    x: (batch, D, L) bf16 or fp32, any strides: channels-first, or the
+    transposed view of a token-major (batch, L, D) tensor; weight (D, W = 2, 3
+    or 4) and bias (D,) fp32; h0 (batch, D, W-1) like x: the inputs before x.
+    Returns (y, last_state): y (batch, D, L) contiguous unless ``out`` says
+    otherwise, as selscan_fwd takes it, and the last W-1 inputs (None unless
+    requested)."""
+    import torch
+    with _on(stream):
+        y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if last_state is None and return_last_state:
+            last_state = torch.empty((x.shape[0], x.shape[1], weight.shape[1] - 1),
+                                     dtype=x.dtype, device=x.device)
+    dev, d = _descs(x, weight, bias, h0, y, last_state)
+    _launch("selscan_conv", dev, stream, *d[:3], int(bool(silu)), *d[3:])
+    return y, last_state
+
+
+def selscan_conv_bwd(x, weight, dy, bias=None, silu=True, h0=None, dlast=None, need_dh0=None,
+                     dx=None, stream=None):
+    """Gradients of selscan_conv for sum(dy * y) + sum(dlast * last_state).
+    Returns a dict: dx (like x, in x's layout unless ``dx`` is given), dweight
+    (D, W) fp32, dbias (D,) fp32 or None, dh0 (batch, D, W-1) like x or None
+    (computed when h0 is given or need_dh0)."""
+    import torch
+    batch, dim, L = x.shape
+    with _on(stream):
+        new = dict(dtype=x.dtype, device=x.device)
+        if dx is None:
+            if x.stride(1) == 1 and x.stride(2) != 1:
+                dx = torch.empty((batch, L, dim), **new).transpose(1, 2)
+            else:
+                dx = torch.empty((batch, dim, L), **new)
+        f32 = dict(dtype=torch.float32, device=x.device)
+        out = {"dx": dx, "dweight": torch.empty(weight.shape, **f32),
+               "dbias": torch.empty((dim,), **f32) if bias is not None else None,
+               "dh0": torch.empty((batch, dim, weight.shape[1] - 1), **new)
+               if (h0 is not None or need_dh0) else None}
+    dev, d = _descs(x, weight, bias, h0, dy, dlast, dx, out["dweight"], out["dbias"], out["dh0"])
+    _launch("selscan_conv_bwd", dev, stream, *d[:3], int(bool(silu)), *d[3:])
+    return out
+
+
+def selscan_conv_step(state, x, weight, bias=None, silu=True, slots=None, out=None, stream=None):
+    """One token of selscan_conv per row; ``state`` (batch, D, W-1) like x
+    is updated in place.  x: (batch, D) (any strides).  With ``slots`` the state
+    is a cache (count, D, W-1), as in selscan_step.  Returns y (batch, D)."""
+    import torch
+    with _on(stream):
+        y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dev, d = _descs(state, slots, x, weight, bias, y)
+    _launch("selscan_conv_step", dev, stream, *d[:5], int(bool(silu)), d[5])
+    return y
+
+
+def selscan_conv_packed(state, x, weight, start, slots, bias=None, silu=True, seen=None,
+                        out=None, stream=None):
+    """selscan_conv over packed prompts of unequal length, through a cache
+    (count, D, W-1) like x of their last inputs, updated in place.  x:
+    (tokens, D), channel stride 1; start, slots and seen as in
+    selscan_fwd_packed.  Returns y (tokens, D)."""
+    import torch
+    with _on(stream):
+        y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dev, d = _descs(state, x, weight, bias, start, slots, seen, y)
+    _launch("selscan_conv_packed", dev, stream, *d[:4], int(bool(silu)), *d[4:])
+    return y
+
+
 def check(stream=None) -> None:
-    """Synchronise ``stream`` and raise if a device-side wait timed out."""
+    """Synchronise ``stream`` and raise if a device-side wait timed out or a
+    slot or sequence was refused on the device."""
     rc = lib().selscan_check(_stream_handle(stream))
     if rc != 0:
         raise SelscanError(rc, "selscan_check")

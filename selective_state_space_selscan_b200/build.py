@@ -13,7 +13,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libselscan.so")
-SOURCES = [os.path.join(CSRC, "selscan_api.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("selscan_api.cu", "layer_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC)
                   if f.endswith((".cuh", ".h"))] + [
     os.path.join(ROOT, "include", f) for f in os.listdir(os.path.join(ROOT, "include"))
@@ -21,7 +21,7 @@ DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC)
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3",
-    "-std=c++17", "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
+    "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
     "--expt-relaxed-constexpr",
 ]
 
@@ -39,11 +39,23 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             and os.path.getmtime(LIB) >= max(os.path.getmtime(p) for p in DEPS)):
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, *extra, "-I", os.path.join(ROOT, "include"),
-           "-I", CSRC, "-o", tmp, *SOURCES, "-lcuda"]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.check_call(cmd)
+    flags = [nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC]
+    objs = [f"{tmp}.{i}.o" for i in range(len(SOURCES))]
+    cmds = [[*flags, *extra, "-c", "-o", o, src] for o, src in zip(objs, SOURCES)]
+    try:
+        jobs = []
+        for cmd in cmds:  # one compiler per source, side by side
+            if verbose:
+                print(" ".join(cmd), file=sys.stderr)
+            jobs.append(subprocess.Popen(cmd))
+        for cmd, rc in [(cmd, job.wait()) for cmd, job in zip(cmds, jobs)]:
+            if rc:
+                raise subprocess.CalledProcessError(rc, cmd)
+        subprocess.check_call([*flags, "-shared", "-o", tmp, *objs, "-lcuda"])
+    finally:
+        for o in objs:
+            if os.path.exists(o):
+                os.remove(o)
     os.replace(tmp, LIB)
     return LIB
 

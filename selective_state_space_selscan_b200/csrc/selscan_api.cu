@@ -14,6 +14,7 @@
 
 #include "selscan.h"
 #include "selscan_debug.h"
+#include "api_common.cuh"
 #include "scan_diag.cuh"
 #include "scan_diag_bf16.cuh"
 #include "ssd_scalarA.cuh"
@@ -29,8 +30,7 @@ __device__ unsigned int g_selscan_err = 0;
 // Kernels launched by this library in this process (selscan_launch_count).
 static std::atomic<unsigned long long> g_launches{0};
 
-// Status of the launch just made; counts it when it succeeded.
-static cudaError_t counted_launch()
+cudaError_t selscan::counted_launch()
 {
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess)
@@ -40,18 +40,14 @@ static cudaError_t counted_launch()
 
 namespace {
 
-constexpr int kMaxDevices = 64;
-
-struct DeviceInfo {
-    bool ready = false;
-    int sm_count = 0;
-    unsigned int *err = nullptr;
-};
-
 std::mutex g_mutex;
 DeviceInfo g_dev[kMaxDevices];
 cudaMemPool_t g_pool[kMaxDevices] = {};  // scratch pools, created on first use
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+}  // namespace
+
+namespace selscan {
 
 unsigned long long default_timeout_ns()
 {
@@ -97,8 +93,7 @@ selscan_status device_setup(int *dev_out, DeviceInfo **info_out)
     return SELSCAN_OK;
 }
 
-// Stream-ordered scratch from a pool of the library's own on the current
-// device.  Its release threshold keeps freed memory mapped: the device's
+// The pool is the library's own on the current device.  Its release threshold keeps freed memory mapped: the device's
 // default pool hands memory back to the driver at every synchronisation, so
 // the next call would map the backward checkpoints (hundreds of MB) again.
 // selscan_release_scratch() trims the pools.
@@ -134,6 +129,10 @@ cudaError_t scratch_alloc(void **p, size_t bytes, cudaStream_t stream)
     }
     return cudaMallocFromPoolAsync(p, bytes, pool, stream);
 }
+
+}  // namespace selscan
+
+namespace {
 
 // Time segments per channel tile of the backward pass: `tiles` units of
 // (batch row, 32 channels), `nchunks` checkpoint chunks, `slots` warps that
@@ -226,80 +225,6 @@ int64_t fwd_segments(int64_t tiles, int64_t chunks, int64_t ctas, int forced_mod
     }
     return tiles <= ctas ? 1 : spread;
 }
-
-size_t elem_size(int32_t dt) { return dt == SELSCAN_BF16 ? 2 : 4; }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int64_t numel(const selscan_tensor *t)
-{
-    int64_t n = 1;
-    for (int i = 0; i < t->ndim && i < 4; ++i)
-        n *= t->shape[i];
-    return n;
-}
-
-// Present: non-NULL descriptor whose data is non-NULL, or that holds no
-// element at all (frameworks hand out NULL data for empty tensors).
-bool present(const selscan_tensor *t)
-{
-    return t && (t->data || (t->ndim >= 1 && t->ndim <= 4 && numel(t) == 0));
-}
-
-// A "sequence" tensor: rank 3 (outer0, outer1, L) with time stride 1 and
-// 16-byte aligned rows, as the bulk tensor copies need.
-selscan_status check_seq(const selscan_tensor *t, int64_t d0, int64_t d1, int64_t L,
-                         int32_t dtype)
-{
-    if (!present(t))
-        return SELSCAN_ERR_NULL;
-    if (t->ndim != 3 || t->shape[0] != d0 || t->shape[1] != d1 || t->shape[2] != L)
-        return SELSCAN_ERR_SHAPE;
-    if (t->dtype != dtype)
-        return SELSCAN_ERR_DTYPE;
-    if (d0 == 0 || d1 == 0 || L == 0)
-        return SELSCAN_OK;  // nothing will be read or written
-    if (L > 1 && t->stride[2] != 1)
-        return SELSCAN_ERR_STRIDE;
-    if (t->stride[0] < 0 || t->stride[1] < 0)
-        return SELSCAN_ERR_STRIDE;
-    const int64_t es = int64_t(elem_size(dtype));
-    if (!aligned16(t->data) || ((t->stride[0] * es) & 15) || ((t->stride[1] * es) & 15))
-        return SELSCAN_ERR_ALIGN;
-    return SELSCAN_OK;
-}
-
-// A small fp32 parameter tensor with the given shape, contiguous.
-selscan_status check_param(const selscan_tensor *t, int ndim, const int64_t *shape,
-                           bool nullable)
-{
-    if (!t || !t->data) {
-        if (nullable)
-            return SELSCAN_OK;
-        if (!present(t))
-            return SELSCAN_ERR_NULL;
-    }
-    if (t->ndim != ndim)
-        return SELSCAN_ERR_SHAPE;
-    int64_t expect = 1, count = 1;
-    for (int i = ndim - 1; i >= 0; --i) {
-        if (t->shape[i] != shape[i])
-            return SELSCAN_ERR_SHAPE;
-        count *= shape[i];
-    }
-    for (int i = ndim - 1; i >= 0 && count > 0; --i) {
-        if (shape[i] > 1 && t->stride[i] != expect)
-            return SELSCAN_ERR_STRIDE;
-        expect *= shape[i];
-    }
-    if (t->dtype != SELSCAN_F32)
-        return SELSCAN_ERR_DTYPE;
-    if ((reinterpret_cast<uintptr_t>(t->data) & 3u) != 0)
-        return SELSCAN_ERR_ALIGN;
-    return SELSCAN_OK;
-}
-
-const void *opt_data(const selscan_tensor *t) { return (t && t->data) ? t->data : nullptr; }
 
 // 3-D tiled map over (L, rows, outer): box (box_t, box_rows, 1), 128-byte
 // swizzle, zero fill outside the tensor.
@@ -553,6 +478,7 @@ const char *selscan_strerror(selscan_status s)
     case SELSCAN_ERR_UNSUPPORTED: return "valid arguments, but this size is not built";
     case SELSCAN_ERR_CUDA: return "CUDA runtime error";
     case SELSCAN_ERR_TIMEOUT: return "a device-side wait timed out";
+    case SELSCAN_ERR_INDEX: return "a slot or a sequence start on the device is not valid";
     }
     return "unknown status";
 }
@@ -605,7 +531,7 @@ selscan_status selscan_check(cudaStream_t stream)
     if (err) {
         const unsigned int zero = 0;
         cudaMemcpyToSymbol(g_selscan_err, &zero, sizeof(zero));
-        return SELSCAN_ERR_TIMEOUT;
+        return err == kErrIndex ? SELSCAN_ERR_INDEX : SELSCAN_ERR_TIMEOUT;
     }
     return SELSCAN_OK;
 }
@@ -1163,75 +1089,25 @@ extern "C" selscan_status selscan_fwd_noalloc(
 // ------------------------------------------------------------ decode step
 namespace {
 
-// A per-token tensor (d0, d1): any non-negative element strides, element-
-// aligned data.
-selscan_status check_tok(const selscan_tensor *t, int64_t d0, int64_t d1, int32_t dtype)
-{
-    if (!present(t))
-        return SELSCAN_ERR_NULL;
-    if (t->ndim != 2 || t->shape[0] != d0 || t->shape[1] != d1)
-        return SELSCAN_ERR_SHAPE;
-    if (t->dtype != dtype)
-        return SELSCAN_ERR_DTYPE;
-    if (d0 == 0 || d1 == 0)
-        return SELSCAN_OK;
-    if (t->stride[0] < 0 || t->stride[1] < 0)
-        return SELSCAN_ERR_STRIDE;
-    if (reinterpret_cast<uintptr_t>(t->data) % elem_size(dtype))
-        return SELSCAN_ERR_ALIGN;
-    return SELSCAN_OK;
-}
-
-// B or C of one token: (batch, N) or (batch, G, N); returns G through *G.
-selscan_status check_tok_bc(const selscan_tensor *t, int64_t batch, int64_t N, int32_t dtype,
-                            int64_t *G, int64_t s[3])
-{
-    if (!present(t))
-        return SELSCAN_ERR_NULL;
-    if (t->dtype != dtype)
-        return SELSCAN_ERR_DTYPE;
-    if (t->ndim == 2) {
-        if (t->shape[0] != batch || t->shape[1] != N)
-            return SELSCAN_ERR_SHAPE;
-        *G = 1;
-        s[0] = t->stride[0];
-        s[1] = 0;
-        s[2] = t->stride[1];
-    } else if (t->ndim == 3) {
-        if (t->shape[0] != batch || t->shape[2] != N || t->shape[1] <= 0)
-            return SELSCAN_ERR_SHAPE;
-        *G = t->shape[1];
-        s[0] = t->stride[0];
-        s[1] = t->stride[1];
-        s[2] = t->stride[2];
-    } else {
-        return SELSCAN_ERR_SHAPE;
-    }
-    if (s[0] < 0 || s[1] < 0 || s[2] < 0)
-        return SELSCAN_ERR_STRIDE;
-    if (numel(t) > 0 && reinterpret_cast<uintptr_t>(t->data) % elem_size(dtype))
-        return SELSCAN_ERR_ALIGN;
-    return SELSCAN_OK;
-}
-
-template <typename T, bool SCALAR>
+template <typename T, bool SCALAR, bool SLOTS>
 cudaError_t launch_step(const StepParams &prm, int64_t batch, int tpc, cudaStream_t stream)
 {
     const int64_t inner = SCALAR ? prm.headdim : prm.dim;
     const dim3 grid(unsigned((inner * tpc + 255) / 256), SCALAR ? unsigned(prm.units) : 1u,
                     unsigned(batch));
     switch (tpc) {
-    case 2: step_kernel<T, 2, SCALAR><<<grid, 256, 0, stream>>>(prm); break;
-    case 4: step_kernel<T, 4, SCALAR><<<grid, 256, 0, stream>>>(prm); break;
-    case 8: step_kernel<T, 8, SCALAR><<<grid, 256, 0, stream>>>(prm); break;
-    default: step_kernel<T, 16, SCALAR><<<grid, 256, 0, stream>>>(prm); break;
+    case 2: step_kernel<T, 2, SCALAR, SLOTS><<<grid, 256, 0, stream>>>(prm); break;
+    case 4: step_kernel<T, 4, SCALAR, SLOTS><<<grid, 256, 0, stream>>>(prm); break;
+    case 8: step_kernel<T, 8, SCALAR, SLOTS><<<grid, 256, 0, stream>>>(prm); break;
+    default: step_kernel<T, 16, SCALAR, SLOTS><<<grid, 256, 0, stream>>>(prm); break;
     }
     return counted_launch();
 }
 
 // Shared by the diagonal and the scalar (Mamba-2) step.  `scalar` selects
-// per-head A / dt / bias / D and a (batch, H, P, N) state.
-selscan_status step_impl(bool scalar, selscan_tensor *state, const selscan_tensor *u,
+// per-head A / dt / bias / D and a (batch, H, P, N) state.  With `slots` the
+// state is a cache (count, ...) and row b works on its slot slots[b].
+selscan_status step_impl(bool scalar, const selscan_tensor *slots, selscan_tensor *state, const selscan_tensor *u,
                          const selscan_tensor *delta, const selscan_tensor *delta_bias,
                          int delta_softplus, const selscan_tensor *A, const selscan_tensor *B,
                          const selscan_tensor *C, const selscan_tensor *D,
@@ -1275,20 +1151,22 @@ selscan_status step_impl(bool scalar, selscan_tensor *state, const selscan_tenso
     if ((st = check_tok_bc(C, batch, N, dt, &Gc, sc)) != SELSCAN_OK) return st;
     if (Gc != G || units % G != 0)
         return SELSCAN_ERR_SHAPE;
+    const int64_t count = slots ? state->shape[0] : batch;
+    if (slots && (st = check_index(slots, batch, false)) != SELSCAN_OK) return st;
     {
         const int64_t ushape[1] = {units};
         if ((st = check_param(delta_bias, 1, ushape, true)) != SELSCAN_OK) return st;
         if ((st = check_param(D, 1, ushape, true)) != SELSCAN_OK) return st;
         if (scalar) {
             if ((st = check_param(A, 1, ushape, false)) != SELSCAN_OK) return st;
-            const int64_t sshape[4] = {batch, units, headdim, N};
+            const int64_t sshape[4] = {count, units, headdim, N};
             if ((st = check_param(state, 4, sshape, false)) != SELSCAN_OK) return st;
         } else {
             const int64_t ashape[2] = {dim, N};
             if ((st = check_param(A, 2, ashape, false)) != SELSCAN_OK) return st;
             if (!aligned16(A->data))
                 return SELSCAN_ERR_ALIGN;
-            const int64_t sshape[3] = {batch, dim, N};
+            const int64_t sshape[3] = {count, dim, N};
             if ((st = check_param(state, 3, sshape, false)) != SELSCAN_OK) return st;
         }
     }
@@ -1299,10 +1177,20 @@ selscan_status step_impl(bool scalar, selscan_tensor *state, const selscan_tenso
     if (!aligned16(state->data))
         return SELSCAN_ERR_ALIGN;
     const int tpc = int(N / 8);
-    if (batch > 65535 || dim * tpc > (int64_t(0x7fffffff) - 255) || units > 65535)
+    if (batch > 65535 || dim * tpc > (int64_t(0x7fffffff) - 255) || units > 65535 ||
+        count > 0x7fffffffll)
         return SELSCAN_ERR_UNSUPPORTED;
 
     StepParams prm{};
+    if (slots) {
+        int dev = 0;
+        DeviceInfo *di = nullptr;
+        if ((st = device_setup(&dev, &di)) != SELSCAN_OK)
+            return st;
+        prm.slots = static_cast<const int *>(slots->data);
+        prm.slot_count = int(count);
+        prm.err = di->err;
+    }
     prm.dim = int(dim);
     prm.headdim = int(headdim);
     prm.units = int(units);
@@ -1343,13 +1231,18 @@ selscan_status step_impl(bool scalar, selscan_tensor *state, const selscan_tenso
     prm.state = static_cast<float *>(state->data);
     prm.softplus = delta_softplus ? 1 : 0;
 
+    const bool bf = dt == SELSCAN_BF16;
     cudaError_t e;
-    if (dt == SELSCAN_BF16)
-        e = scalar ? launch_step<__nv_bfloat16, true>(prm, batch, tpc, stream)
-                   : launch_step<__nv_bfloat16, false>(prm, batch, tpc, stream);
+    if (slots)
+        e = bf ? (scalar ? launch_step<__nv_bfloat16, true, true>(prm, batch, tpc, stream)
+                         : launch_step<__nv_bfloat16, false, true>(prm, batch, tpc, stream))
+               : (scalar ? launch_step<float, true, true>(prm, batch, tpc, stream)
+                         : launch_step<float, false, true>(prm, batch, tpc, stream));
     else
-        e = scalar ? launch_step<float, true>(prm, batch, tpc, stream)
-                   : launch_step<float, false>(prm, batch, tpc, stream);
+        e = bf ? (scalar ? launch_step<__nv_bfloat16, true, false>(prm, batch, tpc, stream)
+                         : launch_step<__nv_bfloat16, false, false>(prm, batch, tpc, stream))
+               : (scalar ? launch_step<float, true, false>(prm, batch, tpc, stream)
+                         : launch_step<float, false, false>(prm, batch, tpc, stream));
     return e == cudaSuccess ? SELSCAN_OK : SELSCAN_ERR_CUDA;
 }
 
@@ -1363,7 +1256,7 @@ extern "C" selscan_status selscan_step(selscan_tensor *state, const selscan_tens
                                        const selscan_tensor *z, selscan_tensor *y,
                                        cudaStream_t stream)
 {
-    return step_impl(false, state, u, delta, delta_bias, delta_softplus, A, B, C, D, z, 1, y,
+    return step_impl(false, nullptr, state, u, delta, delta_bias, delta_softplus, A, B, C, D, z, 1, y,
                      stream);
 }
 
@@ -1375,14 +1268,39 @@ extern "C" selscan_status selscan_step_scalarA(selscan_tensor *state, const sels
                                                const selscan_tensor *z, int64_t headdim,
                                                selscan_tensor *y, cudaStream_t stream)
 {
-    return step_impl(true, state, x, dt, dt_bias, dt_softplus, A, B, C, D, z, headdim, y,
+    return step_impl(true, nullptr, state, x, dt, dt_bias, dt_softplus, A, B, C, D, z, headdim, y,
+                     stream);
+}
+
+extern "C" selscan_status selscan_step_slots(selscan_tensor *state, const selscan_tensor *slots,
+                                             const selscan_tensor *u,
+                                             const selscan_tensor *delta,
+                                             const selscan_tensor *delta_bias,
+                                             int delta_softplus, const selscan_tensor *A,
+                                             const selscan_tensor *B, const selscan_tensor *C,
+                                             const selscan_tensor *D, const selscan_tensor *z,
+                                             selscan_tensor *y, cudaStream_t stream)
+{
+    if (!slots)
+        return SELSCAN_ERR_NULL;
+    return step_impl(false, slots, state, u, delta, delta_bias, delta_softplus, A, B, C, D, z, 1,
+                     y, stream);
+}
+
+extern "C" selscan_status selscan_step_scalarA_slots(
+    selscan_tensor *state, const selscan_tensor *slots, const selscan_tensor *x,
+    const selscan_tensor *dt, const selscan_tensor *dt_bias, int dt_softplus,
+    const selscan_tensor *A, const selscan_tensor *B, const selscan_tensor *C,
+    const selscan_tensor *D, const selscan_tensor *z, int64_t headdim, selscan_tensor *y,
+    cudaStream_t stream)
+{
+    if (!slots)
+        return SELSCAN_ERR_NULL;
+    return step_impl(true, slots, state, x, dt, dt_bias, dt_softplus, A, B, C, D, z, headdim, y,
                      stream);
 }
 
 // ------------------------------------------------------------ backward
-namespace {
-
-}  // namespace
 
 extern "C" selscan_status selscan_bwd(
     const selscan_tensor *u, const selscan_tensor *delta, const selscan_tensor *delta_bias,

@@ -23,6 +23,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "api_common.cuh"
 #include "ptx.cuh"
 #include "scan_diag.cuh"
 
@@ -51,6 +52,10 @@ struct StepParams {
     const float *Dskip;       // (units) or null
     float *state;             // (batch, dim, N) contiguous, updated in place
     int softplus;
+    // SLOTS: the state is (slot_count, dim, N) and row b owns slot slots[b]
+    const int *slots;
+    int slot_count;
+    unsigned int *err;
 };
 
 __device__ __forceinline__ float step_load(const void *base, int64_t off, const float *)
@@ -111,7 +116,14 @@ __device__ __forceinline__ void step_load4(const void *base, int64_t off, int64_
 // TPC: threads per channel (N / 8).  SCALAR: Mamba-2 form.  The fp32
 // instances use the accurate exp / log1p; the bf16 ones the special-function
 // unit (its error is far below bf16 rounding).
-template <typename T, int TPC, bool SCALAR>
+//
+// SLOTS: the rows of a decode batch own scattered slots of a cache.  A row
+// with a negative slot is padding: its block returns and leaves y as it was.
+// A slot past the cache's end, or one that an earlier row of the batch
+// already owns, is refused (the row is skipped and the error word set): two
+// rows on one slot would race on its state.  The block compares the earlier
+// rows' slots itself, 256 per step, from L1.
+template <typename T, int TPC, bool SCALAR, bool SLOTS = false>
 __global__ void __launch_bounds__(256, SCALAR ? 8 : 6) step_kernel(StepParams p)
 {
     constexpr int V = 2;  // 16-byte state vectors per thread
@@ -128,10 +140,26 @@ __global__ void __launch_bounds__(256, SCALAR ? 8 : 6) step_kernel(StepParams p)
     // and the butterfly below stays inside one channel.
     const bool live = cl < (SCALAR ? p.headdim : p.dim);
 
+    int64_t row = b;
+    if (SLOTS) {
+        const int slot = p.slots[b];
+        if (slot < 0)
+            return;
+        bool bad = slot >= p.slot_count;
+        for (int j = int(threadIdx.x); j < b; j += 256)
+            bad |= p.slots[j] == slot;
+        if (__syncthreads_or(bad)) {
+            if (threadIdx.x == 0)
+                atomicOr(p.err, kErrIndex);
+            return;
+        }
+        row = slot;
+    }
+
     float acc = 0.f, x = 0.f;
     if (live) {
         const int g = p.per_group == p.units ? 0 : unit / p.per_group;
-        const int64_t ch = int64_t(b) * p.dim + c;
+        const int64_t ch = row * p.dim + c;
         float4 *sp = reinterpret_cast<float4 *>(p.state + ch * N);
         float4 h[V];
 #pragma unroll
