@@ -11,7 +11,6 @@ pointer, shape and strides.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import struct
@@ -128,6 +127,8 @@ def lib() -> ctypes.CDLL:
         L.selscan_debug_fwd_plan.restype = ctypes.c_longlong
         L.selscan_debug_bwd_plan.argtypes = [ctypes.c_longlong] * 3
         L.selscan_debug_bwd_plan.restype = ctypes.c_longlong
+        L.selscan_debug_packed_segment.argtypes = [ctypes.c_int] * 2
+        L.selscan_debug_packed_segment.restype = None
         _lib = L
     return _lib
 
@@ -183,10 +184,12 @@ def _ref(d):
     return None if d is None else ctypes.byref(d)
 
 
-# selscan_tensor as bytes: a decode step passes ten of them, and packing one
-# takes a fraction of the time of filling a ctypes structure field by field.
+# selscan_tensor as bytes, by rank: a decode step passes ten of them, and
+# packing one takes a fraction of the time of filling a ctypes structure field
+# by field.
 _DESC = struct.Struct("Pii8q")
-_PAD = (0, 0, 0, 0)
+_PACK = (None,) + tuple(struct.Struct(f"=Qii{n}q{32 - 8 * n}x{n}q{32 - 8 * n}x").pack
+                        for n in range(1, 5))
 _CODES: dict = {}
 
 
@@ -197,7 +200,7 @@ def _descs(*tensors):
         import torch
         _CODES.update({torch.float32: SELSCAN_F32, torch.bfloat16: SELSCAN_BF16,
                        torch.int32: SELSCAN_I32})
-    dev, out = None, []
+    dev, out, codes, pack = None, [], _CODES, _PACK
     for t in tensors:
         if t is None:
             out.append(None)
@@ -214,8 +217,7 @@ def _descs(*tensors):
         n = len(shape)
         if not 1 <= n <= 4:
             raise ValueError(f"libselscan takes tensors of 1 to 4 dimensions (got {n})")
-        out.append(_DESC.pack(t.data_ptr(), _CODES.get(t.dtype, -1), n, *shape, *_PAD[n:],
-                              *t.stride(), *_PAD[n:]))
+        out.append(pack[n](t.data_ptr(), codes.get(t.dtype, -1), n, *shape, *t.stride()))
     return dev, out
 
 
@@ -224,27 +226,32 @@ def _launch(name, dev, stream, *args):
     default that device's current stream)."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        # the handle alone: a Stream object costs more than a small kernel
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        handle = raw(dev) if raw else torch.cuda.current_stream(dev).cuda_stream
     elif stream.device_index != dev:
         raise ValueError(f"{name}: the stream is on cuda:{stream.device_index}, the tensors "
                          f"on cuda:{dev}")
+    else:
+        handle = stream.cuda_stream
     f = getattr(lib(), name)
     if torch.cuda.current_device() == dev:
-        rc = f(*args, stream.cuda_stream)
+        rc = f(*args, handle)
     else:
         with torch.cuda.device(dev):
-            rc = f(*args, stream.cuda_stream)
+            rc = f(*args, handle)
     if rc != 0:
         raise SelscanError(rc, name)
 
 
-def _on(stream):
-    """Outputs are allocated on the stream that writes them, so that the
-    allocator does not hand out memory that another stream still uses."""
+def _empty(stream, like, shape, dtype=None):
+    """An output on the stream that writes it, so that the allocator does not
+    hand out memory that another stream still uses."""
     if stream is None:
-        return contextlib.nullcontext()
+        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
     import torch
-    return torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _stream_handle(stream):
@@ -351,8 +358,7 @@ def selscan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=None,
     padding row, whose row of ``out`` is left as it was."""
     import torch
     if slots is not None:
-        with _on(stream):
-            y = out if out is not None else torch.empty(u.shape, dtype=u.dtype, device=u.device)
+        y = out if out is not None else _empty(stream, u, u.shape)
         dev, d = _descs(state, slots, u, delta, delta_bias, A, B, C, D, z, y)
         _launch("selscan_step_slots", dev, stream, *d[:5], int(bool(delta_softplus)), *d[5:])
         return y
@@ -376,8 +382,7 @@ def selscan_step_scalarA(state, x, dt, A, B, C, headdim, D=None, z=None, dt_bias
     cache (count, H, P, N), as in selscan_step."""
     import torch
     if slots is not None:
-        with _on(stream):
-            y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = out if out is not None else _empty(stream, x, x.shape)
         dev, d = _descs(state, slots, x, dt, dt_bias, A, B, C, D, z, y)
         _launch("selscan_step_scalarA_slots", dev, stream, *d[:5], int(bool(dt_softplus)),
                 *d[5:10], int(headdim), d[10])
@@ -483,9 +488,7 @@ def selscan_fwd_packed(state, u, delta, A, B, C, start, slots, D=None, z=None,
     continue their states).  A negative slot marks a padding sequence; its rows
     of ``out``, and rows of no sequence, are left as they were.  Returns y
     (tokens, D)."""
-    import torch
-    with _on(stream):
-        y = out if out is not None else torch.empty(u.shape, dtype=u.dtype, device=u.device)
+    y = out if out is not None else _empty(stream, u, u.shape)
     dev, d = _descs(state, u, delta, delta_bias, A, B, C, D, z, start, slots, seen, y)
     _launch("selscan_fwd_packed", dev, stream, *d[:4], int(bool(delta_softplus)), *d[4:])
     return y
@@ -502,12 +505,9 @@ def selscan_conv(x, weight, bias=None, silu=True, h0=None, out=None, last_state=
     Returns (y, last_state): y (batch, D, L) contiguous unless ``out`` says
     otherwise, as selscan_fwd takes it, and the last W-1 inputs (None unless
     requested)."""
-    import torch
-    with _on(stream):
-        y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if last_state is None and return_last_state:
-            last_state = torch.empty((x.shape[0], x.shape[1], weight.shape[1] - 1),
-                                     dtype=x.dtype, device=x.device)
+    y = out if out is not None else _empty(stream, x, x.shape)
+    if last_state is None and return_last_state:
+        last_state = _empty(stream, x, (x.shape[0], x.shape[1], weight.shape[1] - 1))
     dev, d = _descs(x, weight, bias, h0, y, last_state)
     _launch("selscan_conv", dev, stream, *d[:3], int(bool(silu)), *d[3:])
     return y, last_state
@@ -521,18 +521,16 @@ def selscan_conv_bwd(x, weight, dy, bias=None, silu=True, h0=None, dlast=None, n
     (computed when h0 is given or need_dh0)."""
     import torch
     batch, dim, L = x.shape
-    with _on(stream):
-        new = dict(dtype=x.dtype, device=x.device)
-        if dx is None:
-            if x.stride(1) == 1 and x.stride(2) != 1:
-                dx = torch.empty((batch, L, dim), **new).transpose(1, 2)
-            else:
-                dx = torch.empty((batch, dim, L), **new)
-        f32 = dict(dtype=torch.float32, device=x.device)
-        out = {"dx": dx, "dweight": torch.empty(weight.shape, **f32),
-               "dbias": torch.empty((dim,), **f32) if bias is not None else None,
-               "dh0": torch.empty((batch, dim, weight.shape[1] - 1), **new)
-               if (h0 is not None or need_dh0) else None}
+    if dx is None:
+        if x.stride(1) == 1 and x.stride(2) != 1:
+            dx = _empty(stream, x, (batch, L, dim)).transpose(1, 2)
+        else:
+            dx = _empty(stream, x, (batch, dim, L))
+    f32 = torch.float32
+    out = {"dx": dx, "dweight": _empty(stream, x, weight.shape, f32),
+           "dbias": _empty(stream, x, (dim,), f32) if bias is not None else None,
+           "dh0": _empty(stream, x, (batch, dim, weight.shape[1] - 1))
+           if (h0 is not None or need_dh0) else None}
     dev, d = _descs(x, weight, bias, h0, dy, dlast, dx, out["dweight"], out["dbias"], out["dh0"])
     _launch("selscan_conv_bwd", dev, stream, *d[:3], int(bool(silu)), *d[3:])
     return out
@@ -542,9 +540,7 @@ def selscan_conv_step(state, x, weight, bias=None, silu=True, slots=None, out=No
     """One token of selscan_conv per row; ``state`` (batch, D, W-1) like x
     is updated in place.  x: (batch, D) (any strides).  With ``slots`` the state
     is a cache (count, D, W-1), as in selscan_step.  Returns y (batch, D)."""
-    import torch
-    with _on(stream):
-        y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = out if out is not None else _empty(stream, x, x.shape)
     dev, d = _descs(state, slots, x, weight, bias, y)
     _launch("selscan_conv_step", dev, stream, *d[:5], int(bool(silu)), d[5])
     return y
@@ -556,9 +552,7 @@ def selscan_conv_packed(state, x, weight, start, slots, bias=None, silu=True, se
     (count, D, W-1) like x of their last inputs, updated in place.  x:
     (tokens, D), channel stride 1; start, slots and seen as in
     selscan_fwd_packed.  Returns y (tokens, D)."""
-    import torch
-    with _on(stream):
-        y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = out if out is not None else _empty(stream, x, x.shape)
     dev, d = _descs(state, x, weight, bias, start, slots, seen, y)
     _launch("selscan_conv_packed", dev, stream, *d[:4], int(bool(silu)), *d[4:])
     return y
@@ -599,6 +593,12 @@ def debug_bwd_plan(tiles: int, nchunks: int, slots: int) -> int:
     ``nchunks`` checkpoint chunks and ``slots`` resident warps (host
     arithmetic only, no GPU needed)."""
     return int(lib().selscan_debug_bwd_plan(int(tiles), int(nchunks), int(slots)))
+
+
+def debug_packed_segment(tokens: int, lanes: int = 0) -> None:
+    """Test hook: tokens per segment (0: automatic) and lanes per channel (1 or
+    4, 0: automatic) in selscan_fwd_packed."""
+    lib().selscan_debug_packed_segment(int(tokens), int(lanes))
 
 
 def debug_withhold_carry(unit: int) -> None:

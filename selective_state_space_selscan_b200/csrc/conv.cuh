@@ -148,6 +148,19 @@ __device__ __forceinline__ void load_block(pair_t<T> (&xp)[CH / 2][HLO + TB], co
         return base[c * v.sd + t * v.st];
     };
     if (TOK) {
+        if (v.vec && whole_c && t0 >= HLO && t0 + TB <= L) {
+            const T *r = base + c0 + (t0 - HLO) * v.st;
+#pragma unroll
+            for (int i = 0; i < HLO + TB; ++i) {
+                pair_t<T> w[CH / 2];
+                load_row<T, CH>(r, w);
+                r += v.st;
+#pragma unroll
+                for (int q = 0; q < CH / 2; ++q)
+                    xp[q][i] = w[q];
+            }
+            return;
+        }
         if (v.vec && whole_c && (t0 >= HLO || !past)) {
 #pragma unroll
             for (int i = 0; i < HLO + TB; ++i) {
@@ -214,14 +227,27 @@ __device__ __forceinline__ void load_block(pair_t<T> (&xp)[CH / 2][HLO + TB], co
                                        at(c0 + 2 * q + 1, t0 - HLO + i));
 }
 
-// The block back: pairs yp[channel pair][token], rounded to T.
-template <typename T, bool TOK, int CH, int TB>
-__device__ __forceinline__ void store_block(const pair_t<T> (&yp)[CH / 2][TB], const ConvView &v,
+// The block back: the first TB tokens of the pairs yp[channel pair][token].
+template <typename T, bool TOK, int CH, int TB, int N>
+__device__ __forceinline__ void store_block(const pair_t<T> (&yp)[CH / 2][N], const ConvView &v,
                                             int b, int c0, int t0, int dim, int L)
 {
     constexpr int VEC = 16 / int(sizeof(T));
     T *base = static_cast<T *>(v.data) + b * v.sb;
     if (TOK) {
+        if (v.vec && c0 + CH <= dim && t0 + TB <= L) {
+            T *r = base + c0 + t0 * v.st;
+#pragma unroll
+            for (int i = 0; i < TB; ++i) {
+                pair_t<T> w[CH / 2];
+#pragma unroll
+                for (int q = 0; q < CH / 2; ++q)
+                    w[q] = yp[q][i];
+                store_row<T, CH>(r, w);
+                r += v.st;
+            }
+            return;
+        }
         if (v.vec && c0 + CH <= dim) {
 #pragma unroll
             for (int i = 0; i < TB; ++i)
@@ -276,22 +302,61 @@ __device__ __forceinline__ void store_block(const pair_t<T> (&yp)[CH / 2][TB], c
         }
 }
 
-// Taps and bias of CH channels as pairs (zero past dim).
-template <int W, int CH>
-__device__ __forceinline__ void load_taps(uint64_t (&w)[CH / 2][W], uint64_t (&bias)[CH / 2],
-                                          const float *weight, const float *b, int c0, int dim)
-{
+// The taps and biases of the `n` channels from c0, which a block's four warps
+// share, in shared memory: rows [k][channel], biases in row W (read straight
+// from the weight rows, 32 lanes would touch 32 lines for every element).  The
+// caller synchronises the block.
+template <int W, int CT>
+struct ConvTaps {
+    static constexpr int kPitch = CT + 8;  // a warp's writes fall into different banks
+    float v[W + 1][kPitch];
+    __device__ __forceinline__ void stage(const float *weight, const float *bias, int c0, int n,
+                                          int dim)
+    {
+        const int have = min(n, dim - c0) * W;
+        const float *src = weight + int64_t(c0) * W;
+        const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+        // 16-byte pieces, all of a thread's in flight at once
+        constexpr int PIECES = (CT * W / 4 + 127) / 128;
+        float f[PIECES][4];
 #pragma unroll
-    for (int q = 0; q < CH / 2; ++q) {
-        const int c = c0 + 2 * q;
-        const bool a0 = c < dim, a1 = c + 1 < dim;
+        for (int m = 0; m < PIECES; ++m) {
+            const int i = 4 * (m * 128 + int(threadIdx.x));
+            if (vec && i + 4 <= have) {
+                const float4 x = *reinterpret_cast<const float4 *>(src + i);
+                f[m][0] = x.x;
+                f[m][1] = x.y;
+                f[m][2] = x.z;
+                f[m][3] = x.w;
+            } else {
 #pragma unroll
-        for (int k = 0; k < W; ++k)
-            w[q][k] = pk2(a0 ? weight[int64_t(c) * W + k] : 0.f,
-                          a1 ? weight[int64_t(c + 1) * W + k] : 0.f);
-        bias[q] = pk2(a0 && b ? b[c] : 0.f, a1 && b ? b[c + 1] : 0.f);
+                for (int j = 0; j < 4; ++j)
+                    f[m][j] = i + j < have ? src[i + j] : 0.f;
+            }
+        }
+        for (int i = threadIdx.x; i < n; i += 128)
+            v[W][i] = bias && c0 + i < dim ? bias[c0 + i] : 0.f;
+#pragma unroll
+        for (int m = 0; m < PIECES; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = 4 * (m * 128 + int(threadIdx.x)) + j;
+                if (i < n * W)
+                    v[i % W][i / W] = f[m][j];
+            }
     }
-}
+    // taps and bias of the pair of channels from the block's channel o (even)
+    __device__ __forceinline__ void read(uint64_t (&w)[W], uint64_t &b, int o) const
+    {
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const float2 f = *reinterpret_cast<const float2 *>(&v[k][o]);
+            w[k] = pk2(f.x, f.y);
+        }
+        const float2 f = *reinterpret_cast<const float2 *>(&v[W][o]);
+        b = pk2(f.x, f.y);
+    }
+};
 
 // v sigmoid(v): the special-function unit for bf16 results (its error, about
 // 2^-21, is far below their rounding), the accurate functions for fp32.
@@ -300,8 +365,36 @@ __device__ __forceinline__ uint64_t silu2(uint64_t v)
 {
     if constexpr (std::is_same<T, float>::value)
         return pk2(silu_exact(lo2(v)), silu_exact(hi2(v)));
+    const uint64_t m = mul2(v, pk2(-kLog2e, -kLog2e));
+    const uint64_t d = add2(pk2(ex2_approx(lo2(m)), ex2_approx(hi2(m))), pk2(1.f, 1.f));
+    return mul2(v, pk2(rcp_approx(lo2(d)), rcp_approx(hi2(d))));
+}
+
+// dy times the slope of v sigmoid(v): sg + v sg (1 - sg).
+template <typename T>
+__device__ __forceinline__ uint64_t silu_grad2(uint64_t v, uint64_t dy)
+{
+    uint64_t s;
+    if constexpr (std::is_same<T, float>::value) {
+        s = pk2(1.f / (1.f + expf(-lo2(v))), 1.f / (1.f + expf(-hi2(v))));
+    } else {
+        const uint64_t m = mul2(v, pk2(-kLog2e, -kLog2e));
+        const uint64_t d = add2(pk2(ex2_approx(lo2(m)), ex2_approx(hi2(m))), pk2(1.f, 1.f));
+        s = pk2(rcp_approx(lo2(d)), rcp_approx(hi2(d)));
+    }
+    const uint64_t rest = fma2(s, pk2(-1.f, -1.f), pk2(1.f, 1.f));
+    return mul2(dy, fma2(mul2(v, s), rest, s));
+}
+
+// f(true_type) or f(false_type): a uniform flag tested once instead of at
+// every value.
+template <typename F>
+__device__ __forceinline__ void with_flag(bool flag, F f)
+{
+    if (flag)
+        f(std::true_type());
     else
-        return pk2(silu_fast(lo2(v)), silu_fast(hi2(v)));
+        f(std::false_type());
 }
 
 template <int W>
@@ -343,7 +436,7 @@ __device__ __forceinline__ T conv_tail(const T *x, int64_t st, int L, const T *p
 // of four warps holds four neighbouring token tiles, so that the W-1 rows
 // that a tile reads from the tile before it come from L1.
 template <typename T, int W, bool XTOK, bool YTOK>
-__global__ void __launch_bounds__(128) conv_fwd_kernel(const __grid_constant__ ConvParams p)
+__global__ void __launch_bounds__(128, 5) conv_fwd_kernel(const __grid_constant__ ConvParams p)
 {
     constexpr int CH = 16 / int(sizeof(T)), TB = CH;
     const int lane = threadIdx.x & 31;
@@ -354,35 +447,41 @@ __global__ void __launch_bounds__(128) conv_fwd_kernel(const __grid_constant__ C
     const int tt = (XTOK ? int(blockIdx.x / unsigned(p.ctiles)) : int(blockIdx.x % unsigned(tq))) * 4 +
                    int(threadIdx.x >> 5);
     const int b = int(blockIdx.y);
-    const int c0 = ((ct << p.cg_log2) + cg) * CH;
+    const int cb = (ct << p.cg_log2) * CH, c0 = cb + cg * CH;
     const int64_t tl = (int64_t(tt) * (32 >> p.cg_log2) + tg) * TB;
-    if (c0 >= p.dim || tl >= p.L)
-        return;
-    const int t0 = int(tl);
+    const bool live = c0 < p.dim && tl < p.L;
+    const int t0 = live ? int(tl) : 0;
     const T *past = static_cast<const T *>(p.h0);
-    pair_t<T> xp[CH / 2][W - 1 + TB], yp[CH / 2][TB];
-    load_block<T, XTOK, CH, TB, W - 1>(xp, p.x, past, W - 1, b, c0, t0, p.dim, p.L);
-    uint64_t w[CH / 2][W], bias[CH / 2];
-    load_taps<W, CH>(w, bias, p.weight, p.bias, c0, p.dim);
+    __shared__ __align__(16) ConvTaps<W, 32 * CH> taps;
+    pair_t<T> xp[CH / 2][W - 1 + TB];
+    if (live)
+        load_block<T, XTOK, CH, TB, W - 1>(xp, p.x, past, W - 1, b, c0, t0, p.dim, p.L);
+    taps.stage(p.weight, p.bias, cb, CH << p.cg_log2, p.dim);
+    __syncthreads();
+    if (!live)
+        return;
+    with_flag(p.silu, [&](auto silu) {
 #pragma unroll
-    for (int q = 0; q < CH / 2; ++q) {
-        uint64_t e[W];
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k)
-            e[k + 1] = PairOf<T>::f2(xp[q][k]);
-#pragma unroll
-        for (int i = 0; i < TB; ++i) {
+        for (int q = 0; q < CH / 2; ++q) {
+            uint64_t w[W], bias, e[W];
+            taps.read(w, bias, cg * CH + 2 * q);
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
-                e[k] = e[k + 1];
-            e[W - 1] = PairOf<T>::f2(xp[q][W - 1 + i]);
-            uint64_t v = tap_sum<W>(w[q], e, bias[q]);
-            if (p.silu)
-                v = silu2<T>(v);
-            yp[q][i] = PairOf<T>::round(v);
+                e[k + 1] = PairOf<T>::f2(xp[q][k]);
+#pragma unroll
+            for (int i = 0; i < TB; ++i) {
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k)
+                    e[k] = e[k + 1];
+                e[W - 1] = PairOf<T>::f2(xp[q][W - 1 + i]);
+                uint64_t v = tap_sum<W>(w, e, bias);
+                if (decltype(silu)::value)
+                    v = silu2<T>(v);
+                xp[q][i] = PairOf<T>::round(v);  // in place of an input that is done with
+            }
         }
-    }
-    store_block<T, YTOK, CH, TB>(yp, p.y, b, c0, t0, p.dim, p.L);
+    });
+    store_block<T, YTOK, CH, TB>(xp, p.y, b, c0, t0, p.dim, p.L);
     // The owner of a channel's first tokens is the only reader of its initial
     // state, and writes its final state after that: both may be one buffer.
     if (p.last && t0 == 0) {
@@ -404,6 +503,8 @@ __global__ void __launch_bounds__(128) conv_fwd_kernel(const __grid_constant__ C
 // ------------------------------------------------------- single tokens
 struct ConvStepParams {
     int batch, dim, vec;
+    int wvec;  // the taps may be read as 16-byte pieces
+    int rows;  // of a block
     const void *x;
     int64_t sx0, sx1;
     void *y;
@@ -417,81 +518,157 @@ struct ConvStepParams {
 };
 
 // One token of every row: e = [state | x], the state shifted by one.  A
-// thread owns CH channels of a row, whose (W-1) CH state elements are W-1
-// whole 16-byte vectors (VEC), or one channel (any strides, any dim).
-// Slots as in the scan's decode step: negative is padding, a slot past the
-// end or owned by an earlier row is refused.
-template <typename T, int W, bool VEC>
+// thread owns CH channels, whose (W-1) CH state elements are W-1 whole 16-byte
+// vectors (VEC), or one channel (any strides, any dim), of RB rows at a time:
+// its taps serve all of a block's rows, and the loads of RB rows are in flight
+// at once.  Slots as in the scan's decode step: negative is padding, a slot
+// past the end or owned by an earlier row is refused.
+constexpr int kConvStepRows = 16;  // most rows of a block
+
+template <typename T, int W, bool VEC, int RB>
 __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ ConvStepParams p)
 {
-    constexpr int CH = VEC ? 16 / int(sizeof(T)) : 1;
-    const int b = int(blockIdx.y);
-    int64_t row = b;
+    constexpr int CH = VEC ? 16 / int(sizeof(T)) : 1, NV = W - 1;
+    __shared__ int row_s[kConvStepRows];  // the row's place in the cache, or -1
+    const int tid = threadIdx.x;
+    const int c0 = (int(blockIdx.x) * 128 + tid) * CH;
+    const bool live = c0 < p.dim;
+    const int b0 = int(blockIdx.y) * p.rows, nb = min(p.rows, p.batch - b0);
+    if (tid < nb) {
+        int slot = p.slots ? p.slots[b0 + tid] : b0 + tid;
+        if (slot >= p.slot_count) {
+            atomicOr(p.err, kErrIndex);
+            slot = -1;
+        }
+        row_s[tid] = slot;
+    }
+    // taps [channel][k], as they lie in memory
+    float w[CH * W], bias[CH];
+    if (live) {
+        const float *wr = p.weight + int64_t(c0) * W;
+        if (VEC && p.wvec) {
+#pragma unroll
+            for (int i = 0; i < CH * W / 4; ++i) {
+                const float4 f = reinterpret_cast<const float4 *>(wr)[i];
+                w[4 * i] = f.x;
+                w[4 * i + 1] = f.y;
+                w[4 * i + 2] = f.z;
+                w[4 * i + 3] = f.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < CH * W; ++i)
+                w[i] = wr[i];
+        }
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+            bias[j] = p.bias ? p.bias[c0 + j] : 0.f;
+    }
+    __syncthreads();
+
+    const T *x = static_cast<const T *>(p.x) + c0 * p.sx1;
+    T *y = static_cast<T *>(p.y) + c0 * p.sy1;
+    T *state = static_cast<T *>(p.state) + int64_t(c0) * NV;
+    struct Rows {
+        alignas(16) T raw[RB][NV * CH];
+        alignas(16) T x[RB][CH];
+    };
+    const auto load = [&](Rows &r, int i0) {
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+            const int row = i0 + i < nb ? row_s[i0 + i] : -1;
+            if (row < 0 || !live)
+                continue;
+            const T *st = state + int64_t(row) * p.dim * NV;
+            const T *xi = x + (b0 + i0 + i) * p.sx0;
+            if constexpr (VEC) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    *reinterpret_cast<uint4 *>(r.raw[i] + k * CH) =
+                        reinterpret_cast<const uint4 *>(st)[k];
+                *reinterpret_cast<uint4 *>(r.x[i]) = *reinterpret_cast<const uint4 *>(xi);
+            } else {
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    r.raw[i][k] = st[k];
+                r.x[i][0] = xi[0];
+            }
+        }
+    };
+    const auto step = [&](const Rows &r, int i0) {
+#pragma unroll
+        for (int i = 0; i < RB; ++i) {
+            const int row = i0 + i < nb ? row_s[i0 + i] : -1;
+            if (row < 0)
+                continue;
+            alignas(16) T yr[CH], sr[NV * CH];
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                float v = bias[j];
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    v = fmaf(w[j * W + k], float(r.raw[i][j * NV + k]), v);
+                v = fmaf(w[j * W + NV], float(r.x[i][j]), v);
+                if (p.silu)
+                    v = std::is_same<T, float>::value ? silu_exact(v) : silu_fast(v);
+                yr[j] = T(v);
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    sr[j * NV + k] = k + 1 < NV ? r.raw[i][j * NV + (k + 1 < NV ? k + 1 : 0)] : r.x[i][j];
+            }
+            T *st = state + int64_t(row) * p.dim * NV;
+            T *yi = y + (b0 + i0 + i) * p.sy0;
+            if constexpr (VEC) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    reinterpret_cast<uint4 *>(st)[k] = *reinterpret_cast<uint4 *>(sr + k * CH);
+                *reinterpret_cast<uint4 *>(yi) = *reinterpret_cast<uint4 *>(yr);
+            } else {
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    st[k] = sr[k];
+                yi[0] = yr[0];
+            }
+        }
+    };
+    Rows ra, rb;
+    load(ra, 0);
+
     if (p.slots) {
-        const int slot = p.slots[b];
-        if (slot < 0)
-            return;
-        bool bad = slot >= p.slot_count;
-        for (int j = int(threadIdx.x); j < b; j += 128)
-            bad |= p.slots[j] == slot;
-        if (__syncthreads_or(bad)) {
-            if (threadIdx.x == 0)
+        // earlier rows with one of this block's slots, eight loads at a time
+        unsigned bad = 0;
+        for (int j0 = tid; j0 < b0 + nb - 1; j0 += 8 * 128) {
+            int other[8];
+#pragma unroll
+            for (int m = 0; m < 8; ++m)
+                other[m] = j0 + m * 128 < b0 + nb - 1 ? p.slots[j0 + m * 128] : -1;
+            for (int i = 0; i < nb; ++i) {
+                const int mine = row_s[i];
+#pragma unroll
+                for (int m = 0; m < 8; ++m)
+                    if (other[m] >= 0 && other[m] == mine && j0 + m * 128 < b0 + i)
+                        bad |= 1u << i;
+            }
+        }
+        __syncthreads();
+        for (int i = 0; bad && i < nb; ++i)
+            if (bad >> i & 1) {
+                row_s[i] = -1;
                 atomicOr(p.err, kErrIndex);
-            return;
-        }
-        row = slot;
+            }
+        __syncthreads();
     }
-    const int c0 = (int(blockIdx.x) * 128 + int(threadIdx.x)) * CH;
-    if (c0 >= p.dim)
+    if (!live)
         return;
-    T e[CH][W];
-    T *st = static_cast<T *>(p.state) + (row * p.dim + c0) * (W - 1);
-    const T *x = static_cast<const T *>(p.x) + b * p.sx0 + c0 * p.sx1;
-    if constexpr (VEC) {
-        alignas(16) T raw[(W - 1) * CH];
-        alignas(16) T xr[CH];
-#pragma unroll
-        for (int i = 0; i < W - 1; ++i)
-            *reinterpret_cast<uint4 *>(raw + i * CH) = reinterpret_cast<const uint4 *>(st)[i];
-        *reinterpret_cast<uint4 *>(xr) = *reinterpret_cast<const uint4 *>(x);
-#pragma unroll
-        for (int j = 0; j < CH; ++j) {
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k)
-                e[j][k] = raw[j * (W - 1) + k];
-            e[j][W - 1] = xr[j];
+    // the next rows are on their way while these are worked on
+    for (int i0 = 0; i0 < nb; i0 += 2 * RB) {
+        if (p.rows > RB)
+            load(rb, i0 + RB);
+        step(ra, i0);
+        if (p.rows > RB) {
+            load(ra, i0 + 2 * RB);
+            step(rb, i0 + RB);
         }
-    } else {
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k)
-            e[0][k] = st[k];
-        e[0][W - 1] = x[0];
-    }
-    alignas(16) T yr[CH], sr[(W - 1) * CH];
-#pragma unroll
-    for (int j = 0; j < CH; ++j) {
-        float v = p.bias ? p.bias[c0 + j] : 0.f;
-#pragma unroll
-        for (int k = 0; k < W; ++k)
-            v = fmaf(p.weight[int64_t(c0 + j) * W + k], float(e[j][k]), v);
-        if (p.silu)
-            v = std::is_same<T, float>::value ? silu_exact(v) : silu_fast(v);
-        yr[j] = T(v);
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k)
-            sr[j * (W - 1) + k] = e[j][k + 1];
-    }
-    T *y = static_cast<T *>(p.y) + b * p.sy0 + c0 * p.sy1;
-    if constexpr (VEC) {
-#pragma unroll
-        for (int i = 0; i < W - 1; ++i)
-            reinterpret_cast<uint4 *>(st)[i] = *reinterpret_cast<uint4 *>(sr + i * CH);
-        *reinterpret_cast<uint4 *>(y) = *reinterpret_cast<uint4 *>(yr);
-    } else {
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k)
-            st[k] = sr[k];
-        y[0] = yr[0];
     }
 }
 
@@ -513,51 +690,93 @@ struct PackedSeq {
     bool fresh;
 };
 
-// The last sequence that does not begin behind `key`, where sequence i begins
-// at start[i] / div + i * mul (a non-decreasing map), by the whole warp: 32
-// probes a step.
-__device__ __forceinline__ int packed_find(const PackedIndex &ix, int64_t key, int div, int mul,
-                                           int lane)
-{
-    int lo = 0, hi = ix.seqs;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32;
-        const int i = lo + lane * step;
-        const bool le = i < hi && int64_t(ix.start[i]) / div + int64_t(i) * mul <= key;
-        const unsigned m = __ballot_sync(0xffffffffu, le);
-        const int k = m ? 31 - __clz(m) : 0;
-        lo += k * step;
-        hi = min(hi, lo + step);
-    }
-    return lo;
-}
+// A warp's view of the sequences.  Up to 32 of them are held one per lane, all
+// their numbers loaded at once, so that finding and checking one costs no
+// further trip to memory; more are searched 32 probes a step.
+struct PackedView {
+    const PackedIndex &ix;
+    int lane;
+    int begin_, end_, slot_, seen_;  // of sequence `lane` (few sequences)
 
-// Sequence s as the warp may work on it: false for padding (a negative slot)
-// and for one that is refused, which sets the error word: rows outside the
-// buffer, a slot past the cache's end, or a slot that an earlier sequence
-// owns (two owners would race on its state).
-__device__ __forceinline__ bool packed_seq(const PackedIndex &ix, int s, int lane, PackedSeq &q)
-{
-    q.begin = ix.start[s];
-    q.end = ix.start[s + 1];
-    q.slot = ix.slots[s];
-    q.fresh = ix.seen && ix.seen[s] <= 0;
-    if (q.slot < 0)
-        return false;
-    bool bad = q.begin < 0 || q.end < q.begin || q.end > ix.tokens || q.slot >= ix.slot_count;
-    for (int j = lane; j < s; j += 32)
-        bad |= ix.slots[j] == q.slot;
-    if (__any_sync(0xffffffffu, bad)) {
-        if (lane == 0)
-            atomicOr(ix.err, kErrIndex);
-        return false;
+    __device__ __forceinline__ PackedView(const PackedIndex &i, int l) : ix(i), lane(l)
+    {
+        if (lane < ix.seqs && ix.seqs <= 32) {
+            begin_ = ix.start[lane];
+            end_ = ix.start[lane + 1];
+            slot_ = ix.slots[lane];
+            seen_ = ix.seen ? ix.seen[lane] : 1;
+        } else {
+            begin_ = end_ = seen_ = 0;
+            slot_ = -1;
+        }
     }
-    return true;
-}
+
+    // The last sequence that does not begin behind `key`, where sequence i
+    // begins at start[i] / div + i * mul (a non-decreasing map); 0 if all do.
+    __device__ __forceinline__ int find(int64_t key, int div, int mul) const
+    {
+        if (ix.seqs <= 32) {
+            const bool le = lane < ix.seqs && int64_t(begin_) / div + int64_t(lane) * mul <= key;
+            const unsigned m = __ballot_sync(0xffffffffu, le);
+            return m ? 31 - __clz(m) : 0;
+        }
+        int lo = 0, hi = ix.seqs;
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32;
+            const int i = lo + lane * step;
+            const bool le = i < hi && int64_t(ix.start[i]) / div + int64_t(i) * mul <= key;
+            const unsigned m = __ballot_sync(0xffffffffu, le);
+            const int k = m ? 31 - __clz(m) : 0;
+            lo += k * step;
+            hi = min(hi, lo + step);
+        }
+        return lo;
+    }
+
+    // Where sequence s begins.
+    __device__ __forceinline__ int begin(int s) const
+    {
+        return ix.seqs <= 32 ? __shfl_sync(0xffffffffu, begin_, s & 31) : ix.start[s];
+    }
+
+    // Sequence s as the warp may work on it: false for padding (a negative
+    // slot) and for one that is refused, which sets the error word: rows
+    // outside the buffer, a slot past the cache's end, or a slot that an
+    // earlier sequence owns (two owners would race on its state).
+    __device__ __forceinline__ bool get(int s, PackedSeq &q) const
+    {
+        bool bad = false;
+        if (ix.seqs <= 32) {
+            q.begin = __shfl_sync(0xffffffffu, begin_, s);
+            q.end = __shfl_sync(0xffffffffu, end_, s);
+            q.slot = __shfl_sync(0xffffffffu, slot_, s);
+            q.fresh = __shfl_sync(0xffffffffu, seen_, s) <= 0;
+            bad = lane < s && slot_ == q.slot;
+        } else {
+            q.begin = ix.start[s];
+            q.end = ix.start[s + 1];
+            q.slot = ix.slots[s];
+            q.fresh = ix.seen && ix.seen[s] <= 0;
+#pragma unroll 4
+            for (int j = lane; j < s; j += 32)
+                bad |= ix.slots[j] == q.slot;
+        }
+        if (q.slot < 0)
+            return false;
+        bad |= q.begin < 0 || q.end < q.begin || q.end > ix.tokens || q.slot >= ix.slot_count;
+        if (__any_sync(0xffffffffu, bad)) {
+            if (lane == 0)
+                atomicOr(ix.err, kErrIndex);
+            return false;
+        }
+        return true;
+    }
+};
 
 struct ConvPackedParams {
     PackedIndex ix;
     int dim, vec, runs, ctiles;
+    int svec;  // the state may be read and written as 16-byte pieces
     const void *x;
     int64_t sx;  // row stride; channels are contiguous
     void *y;
@@ -569,21 +788,121 @@ struct ConvPackedParams {
 
 constexpr int kConvRun = 8;  // rows of a warp
 
-// A warp owns kConvRun rows x 32 CH channels.  The usual warp lies inside one
-// sequence, W-1 rows or more behind its first: it loads its rows and the W-1
-// before them and is done.  The others go token by token.  A sequence's first
-// W-1 tokens, which need the old state, are all taken by the warp that holds
-// its first row, which also writes the new state: no other warp touches the
-// slot.  One more warp (run == runs) looks after sequences without rows.
-template <typename T, int W, bool VEC>
-__global__ void __launch_bounds__(128) conv_packed_kernel(const __grid_constant__ ConvPackedParams p)
+// A warp owns kConvRun rows x 32 CH channels; a block's four warps take
+// neighbouring runs of the same channels.  The rows and the W-1 before them
+// are loaded before the warp knows whose they are; then it walks the sequences
+// in its rows.  A sequence's first W-1 tokens, which
+// need the old state, are all taken by the warp that holds its first row
+// (packed_head), which also writes the new state: no other warp touches the
+// slot.  The other tokens are computed from the loaded rows, under a mask.
+// One more warp (run == runs) looks after sequences without rows.
+//
+// packed_head: sequence q's first W-1 tokens and its new state, of CH channels
+// from c0.  state: the slot's row, whose (W-1) CH elements of these channels
+// are W-1 whole vectors where svec says so.
+template <typename T, int W, bool VEC, int CH>
+__device__ __forceinline__ void packed_head(const PackedSeq &q, int c0, int dim, const T *xb,
+                                            int64_t sx, T *yb, int64_t sy, T *state, bool svec,
+                                            const ConvTaps<W, 32 * CH> &taps, int o, int silu)
 {
-    constexpr int CH = VEC ? 16 / int(sizeof(T)) : 2;
+    constexpr int H = W - 1;
+    const T zero = conv_zero(static_cast<const T *>(nullptr));
+    alignas(16) T old[CH * H], first[H][CH], tail[H][CH], out[CH * H];
+    const int chans = min(CH, dim - c0);
+    const auto row = [&](int t, T(&v)[CH]) {
+        if (VEC) {
+            *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(xb + int64_t(t) * sx + c0);
+        } else {
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+                v[j] = j < chans ? xb[int64_t(t) * sx + c0 + j] : zero;
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < H; ++k) {
+        if (svec && !q.fresh) {
+            *reinterpret_cast<uint4 *>(old + k * (16 / int(sizeof(T)))) =
+                reinterpret_cast<const uint4 *>(state)[k];
+        } else {
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+                old[j * H + k] = q.fresh || j >= chans ? zero : state[j * H + k];
+        }
+        if (q.begin + k < q.end)
+            row(q.begin + k, first[k]);
+        if (q.end - H + k >= q.begin)
+            row(q.end - H + k, tail[k]);
+    }
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+        if (q.begin + i >= q.end)
+            break;
+        T yv[CH];
+#pragma unroll
+        for (int r = 0; r < CH / 2; ++r) {
+            uint64_t w[W], bias, e[W];
+            taps.read(w, bias, o + 2 * r);
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+                const int pos = i - H + k;  // place in the sequence
+                e[k] = pos >= 0 ? pk2(float(first[pos >= 0 ? pos : 0][2 * r]),
+                                      float(first[pos >= 0 ? pos : 0][2 * r + 1]))
+                                : pk2(float(old[2 * r * H + (pos < 0 ? H + pos : 0)]),
+                                      float(old[(2 * r + 1) * H + (pos < 0 ? H + pos : 0)]));
+            }
+            uint64_t v = tap_sum<W>(w, e, bias);
+            if (silu)
+                v = silu2<T>(v);
+            const pair_t<T> o = PairOf<T>::round(v);
+            yv[2 * r] = PairOf<T>::lo(o);
+            yv[2 * r + 1] = PairOf<T>::hi(o);
+        }
+        T *y = yb + int64_t(q.begin + i) * sy + c0;
+        if (VEC) {
+            *reinterpret_cast<uint4 *>(y) = *reinterpret_cast<uint4 *>(yv);
+        } else {
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+                if (j < chans)
+                    y[j] = yv[j];
+        }
+    }
+    const int len = q.end - q.begin;
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int k = 0; k < H; ++k) {
+            // input len - H + k, one of the old state's where that is negative
+            T v = tail[k][j];
+#pragma unroll
+            for (int l = 1; l < H; ++l)
+                if (len == l && k + l < H)
+                    v = old[j * H + (k + l < H ? k + l : 0)];
+            out[j * H + k] = v;
+        }
+#pragma unroll
+    for (int k = 0; k < H; ++k) {
+        if (svec) {
+            reinterpret_cast<uint4 *>(state)[k] =
+                *reinterpret_cast<uint4 *>(out + k * (16 / int(sizeof(T))));
+        } else {
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+                if (j < chans)
+                    state[j * H + k] = out[j * H + k];
+        }
+    }
+}
+
+template <typename T, int W, bool VEC>
+__global__ void __launch_bounds__(128, 5) conv_packed_kernel(const __grid_constant__ ConvPackedParams p)
+{
+    constexpr int CH = VEC ? 16 / int(sizeof(T)) : 4, H = W - 1;
+    __shared__ __align__(16) ConvTaps<W, 32 * CH> taps;
     const int lane = threadIdx.x & 31;
-    const int64_t wid = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int ct = int(wid % p.ctiles), run = int(wid / p.ctiles);
-    if (run > p.runs)
-        return;
+    const int ct = int(blockIdx.x % unsigned(p.ctiles));
+    const int64_t run64 = int64_t(blockIdx.x / unsigned(p.ctiles)) * 4 + (threadIdx.x >> 5);
+    const int run = int(min(run64, int64_t(p.runs) + 1));
     const PackedIndex &ix = p.ix;
     const int c0 = (ct * 32 + lane) * CH;
     const bool live = c0 < p.dim;
@@ -591,6 +910,41 @@ __global__ void __launch_bounds__(128) conv_packed_kernel(const __grid_constant_
     T *yb = static_cast<T *>(p.y);
     T *state = static_cast<T *>(p.state);
     const T zero = conv_zero(static_cast<const T *>(nullptr));
+
+    const int t0 = run * kConvRun, t1 = min(t0 + kConvRun, ix.tokens);
+    const auto fetch = [&](int t, pair_t<T>(&v)[CH / 2]) {
+        if (!live || t < 0 || t >= t1) {
+#pragma unroll
+            for (int r = 0; r < CH / 2; ++r)
+                v[r] = 0;
+        } else if (VEC) {
+            load_row<T, CH>(xb + int64_t(t) * p.sx + c0, v);
+        } else {
+            const T *x = xb + int64_t(t) * p.sx + c0;
+#pragma unroll
+            for (int r = 0; r < CH / 2; ++r)
+                v[r] = PairOf<T>::make(c0 + 2 * r < p.dim ? x[2 * r] : zero,
+                                       c0 + 2 * r + 1 < p.dim ? x[2 * r + 1] : zero);
+        }
+    };
+    pair_t<T> xp[H + kConvRun][CH / 2];
+    if (VEC && live && run < p.runs && t0 >= H && t0 + kConvRun <= ix.tokens) {
+        const T *x = xb + int64_t(t0 - H) * p.sx + c0;
+#pragma unroll
+        for (int i = 0; i < H + kConvRun; ++i) {
+            load_row<T, CH>(x, xp[i]);
+            x += p.sx;
+        }
+    } else if (run < p.runs) {
+#pragma unroll
+        for (int i = 0; i < H + kConvRun; ++i)
+            fetch(t0 - H + i, xp[i]);
+    }
+    const PackedView view(ix, lane);
+    taps.stage(p.weight, p.bias, ct * 32 * CH, 32 * CH, p.dim);
+    __syncthreads();
+    if (run > p.runs)
+        return;
 
     if (run == p.runs) {
         for (int s0 = 0; s0 < ix.seqs; s0 += 32) {
@@ -608,100 +962,86 @@ __global__ void __launch_bounds__(128) conv_packed_kernel(const __grid_constant_
                 const int i = s0 + __ffs(m) - 1;
                 m &= m - 1;
                 PackedSeq q;
-                if (!packed_seq(ix, i, lane, q) || !live)
+                if (!view.get(i, q) || !live)
                     continue;
                 for (int j = 0; j < CH && c0 + j < p.dim; ++j)
-                    for (int k = 0; k < W - 1; ++k)
-                        state[(int64_t(q.slot) * p.dim + c0 + j) * (W - 1) + k] = zero;
+                    for (int k = 0; k < H; ++k)
+                        state[(int64_t(q.slot) * p.dim + c0 + j) * H + k] = zero;
             }
         }
         return;
     }
 
-    const int t0 = run * kConvRun, t1 = min(t0 + kConvRun, ix.tokens);
-    int s = packed_find(ix, t0, 1, 0, lane);
-    PackedSeq q;
-    bool ok = packed_seq(ix, s, lane, q);
-    uint64_t w[CH / 2][W], bias[CH / 2];
-    load_taps<W, CH>(w, bias, p.weight, p.bias, live ? c0 : p.dim, p.dim);
-
-    if (VEC && ok && q.begin + (W - 1) <= t0 && q.end >= t1 && t1 - t0 == kConvRun) {
-        if (!live)
-            return;
-        pair_t<T> xp[W - 1 + kConvRun][CH / 2];
+    // the sequences in this run: which rows are behind a head, and whether any
+    // sequence begins here
+    unsigned mask = 0;
+    bool heads = false;
+    const int s0 = view.find(t0, 1, 0);
+    for (int s = s0; s < ix.seqs && view.begin(s) < t1; ++s) {
+        PackedSeq q;
+        if (!view.get(s, q) || q.begin >= q.end)
+            continue;
+        const int lo = max(t0, min(q.end, q.begin + H)) - t0, hi = min(t1, q.end) - t0;
+        if (lo < hi)
+            mask |= (1u << hi) - (1u << lo);
+        heads |= q.begin >= t0;
+    }
+    // pair by pair of channels; the outputs take the places of the inputs
+    with_flag(p.silu, [&](auto silu) {
 #pragma unroll
-        for (int i = 0; i < W - 1 + kConvRun; ++i)
-            load_row<T, CH>(xb + int64_t(t0 - (W - 1) + i) * p.sx + c0, xp[i]);
+        for (int r = 0; r < CH / 2; ++r) {
+            uint64_t w[W], bias, e[W];
+            taps.read(w, bias, lane * CH + 2 * r);
+#pragma unroll
+            for (int k = 0; k < H; ++k)
+                e[k + 1] = PairOf<T>::f2(xp[k][r]);
+#pragma unroll
+            for (int i = 0; i < kConvRun; ++i) {
+#pragma unroll
+                for (int k = 0; k < H; ++k)
+                    e[k] = e[k + 1];
+                e[H] = PairOf<T>::f2(xp[H + i][r]);
+                uint64_t v = tap_sum<W>(w, e, bias);
+                if (decltype(silu)::value)
+                    v = silu2<T>(v);
+                xp[i][r] = PairOf<T>::round(v);
+            }
+        }
+    });
+    if (VEC && live && mask == (1u << kConvRun) - 1) {
+        T *y = yb + int64_t(t0) * p.sy + c0;
 #pragma unroll
         for (int i = 0; i < kConvRun; ++i) {
-            pair_t<T> out[CH / 2];
-#pragma unroll
-            for (int r = 0; r < CH / 2; ++r) {
-                uint64_t e[W];
-#pragma unroll
-                for (int k = 0; k < W; ++k)
-                    e[k] = PairOf<T>::f2(xp[i + k][r]);
-                uint64_t v = tap_sum<W>(w[r], e, bias[r]);
-                if (p.silu)
-                    v = silu2<T>(v);
-                out[r] = PairOf<T>::round(v);
-            }
-            store_row<T, CH>(yb + int64_t(t0 + i) * p.sy + c0, out);
+            store_row<T, CH>(y, xp[i]);
+            y += p.sy;
         }
-        return;
+    } else if (live) {
+#pragma unroll
+        for (int i = 0; i < kConvRun; ++i) {
+            if (!(mask >> i & 1))
+                continue;
+            T *y = yb + int64_t(t0 + i) * p.sy + c0;
+            if (VEC) {
+                store_row<T, CH>(y, xp[i]);
+            } else {
+#pragma unroll
+                for (int r = 0; r < CH / 2; ++r) {
+                    if (c0 + 2 * r < p.dim)
+                        y[2 * r] = PairOf<T>::lo(xp[i][r]);
+                    if (c0 + 2 * r + 1 < p.dim)
+                        y[2 * r + 1] = PairOf<T>::hi(xp[i][r]);
+                }
+            }
+        }
     }
-
-    for (;;) {
-        if (ok && q.begin < q.end) {
-            const bool mine = q.begin >= t0 && q.begin < t1;
-            const int lo = mine ? q.begin : max(t0, min(q.end, q.begin + W - 1));
-            const int hi = mine ? max(min(t1, q.end), min(q.end, q.begin + W - 1))
-                                : min(t1, q.end);
-            if (live) {
-                const int64_t srow = (int64_t(q.slot) * p.dim + c0) * (W - 1);
-                // element t of the sequence's input behind its past, channel c0 + j
-                const auto at = [&](int t, int j) -> T {
-                    if (c0 + j >= p.dim)
-                        return zero;
-                    if (t >= q.begin)
-                        return xb[int64_t(t) * p.sx + c0 + j];
-                    return q.fresh ? zero : state[srow + j * (W - 1) + W - 1 + (t - q.begin)];
-                };
-                for (int t = lo; t < hi; ++t) {
-#pragma unroll
-                    for (int r = 0; r < CH / 2; ++r) {
-                        uint64_t e[W];
-#pragma unroll
-                        for (int k = 0; k < W; ++k)
-                            e[k] = PairOf<T>::f2(PairOf<T>::make(at(t - (W - 1) + k, 2 * r),
-                                                                 at(t - (W - 1) + k, 2 * r + 1)));
-                        uint64_t v = tap_sum<W>(w[r], e, bias[r]);
-                        if (p.silu)
-                            v = silu2<T>(v);
-                        const pair_t<T> o = PairOf<T>::round(v);
-                        T *y = yb + int64_t(t) * p.sy + c0 + 2 * r;
-                        if (c0 + 2 * r < p.dim)
-                            y[0] = PairOf<T>::lo(o);
-                        if (c0 + 2 * r + 1 < p.dim)
-                            y[1] = PairOf<T>::hi(o);
-                    }
-                }
-                if (mine) {
-                    for (int j = 0; j < CH && c0 + j < p.dim; ++j) {
-                        T tail[W - 1];
-#pragma unroll
-                        for (int k = 0; k < W - 1; ++k)
-                            tail[k] = at(q.end - (W - 1) + k, j);
-#pragma unroll
-                        for (int k = 0; k < W - 1; ++k)
-                            state[srow + j * (W - 1) + k] = tail[k];
-                    }
-                }
-            }
-        }
-        if (++s >= ix.seqs || ix.start[s] >= t1)
-            break;
-        ok = packed_seq(ix, s, lane, q);
+    if (!heads)
+        return;
+    for (int s = s0; s < ix.seqs && view.begin(s) < t1; ++s) {
+        PackedSeq q;
+        if (view.get(s, q) && q.begin < q.end && q.begin >= t0 && live)
+            packed_head<T, W, VEC, CH>(q, c0, p.dim, xb, p.sx, yb, p.sy,
+                                       state + (int64_t(q.slot) * p.dim + c0) * H, p.svec, taps,
+                                       lane * CH, p.silu);
     }
 }
 
@@ -725,143 +1065,152 @@ struct ConvBwdParams {
 // the tokens behind its own: those of the lane that holds the next token
 // block (a shuffle), or, for the warp's last block, of the first block of the
 // tile done before.  Above a run they are recomputed: the run's first step is
-// the tile behind it, of which only those W-1 tokens are formed.
+// the block behind it, of which only those W-1 tokens are used.
 template <typename T, int W, bool XTOK, bool YTOK>
-__global__ void __launch_bounds__(128) conv_bwd_kernel(const __grid_constant__ ConvBwdParams p)
+__global__ void __launch_bounds__(128, 4) conv_bwd_kernel(const __grid_constant__ ConvBwdParams p)
 {
     constexpr int CH = 4, TB = 16 / int(sizeof(T)), Q = CH / 2, H = W - 1;
+    __shared__ __align__(16) ConvTaps<W, 32 * CH> taps;
     const int lane = threadIdx.x & 31;
     const int ngr = 32 >> p.cg_log2;  // token blocks of a tile
     const int cg = lane & ((1 << p.cg_log2) - 1), tg = lane >> p.cg_log2;
-    const int64_t wid = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int ct = int(wid % p.ctiles), run = int(wid / p.ctiles);
-    if (run >= p.runs)
-        return;
+    // a block's warps take neighbouring runs of the same channels
+    const int ct = int(blockIdx.x % unsigned(p.ctiles));
+    const int run = int(blockIdx.x / unsigned(p.ctiles)) * 4 + int(threadIdx.x >> 5);
     const int b = int(blockIdx.y);
-    const int c0 = ((ct << p.cg_log2) + cg) * CH;
+    const int cb = (ct << p.cg_log2) * CH, c0 = cb + cg * CH;
     const int tile = ngr * TB;
     const T *past = static_cast<const T *>(p.h0);
-    uint64_t w[Q][W], bias[Q], dw[Q][W], db[Q];
-    load_taps<W, CH>(w, bias, p.weight, p.bias, c0, p.dim);
+    taps.stage(p.weight, p.bias, cb, CH << p.cg_log2, p.dim);
+    __syncthreads();
+    if (run >= p.runs)
+        return;
+    uint64_t dw[Q][W], db[Q];
+    uint64_t head[Q][H];  // this block's first W-1 g of the tile done before
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         db[q] = 0;
 #pragma unroll
         for (int k = 0; k < W; ++k)
             dw[q][k] = 0;
-    }
-    uint64_t head[Q][H];  // this block's first W-1 g of the tile done before
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
 #pragma unroll
         for (int k = 0; k < H; ++k)
             head[q][k] = 0;
+    }
 
     const int64_t first = int64_t(run) * p.steps * tile;
     for (int step = p.steps; step >= 0; --step) {
         const int64_t tl = first + int64_t(step) * tile;  // the tile's first token
         if (tl >= p.L)
             continue;  // nothing there: g is zero (uniform over the warp)
-        const int t0 = int(min(tl + int64_t(tg) * TB, int64_t(p.L)));
-        const bool above = step == p.steps;  // the tile behind the run
+        const bool above = step == p.steps;  // the block behind the run
+        const int t0 = above && tg ? p.L : int(min(tl + int64_t(tg) * TB, int64_t(p.L)));
         pair_t<T> xp[Q][H + TB], yp[Q][TB];
-        load_block<T, XTOK, CH, TB, H>(xp, p.x, past, H, b, c0, t0, p.dim, p.L);
-        load_block<T, YTOK, CH, TB, 0>(yp, p.dy, nullptr, 0, b, c0, t0, p.dim, p.L);
-        uint64_t g[Q][TB + H];
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-#pragma unroll
-            for (int i = 0; i < TB; ++i) {
-                uint64_t e[W];
-#pragma unroll
-                for (int k = 0; k < W; ++k)
-                    e[k] = PairOf<T>::f2(xp[q][i + k]);
-                const uint64_t dy = PairOf<T>::f2(yp[q][i]);
-                uint64_t gv = dy;
-                if (p.silu) {
-                    const uint64_t v = tap_sum<W>(w[q], e, bias[q]);
-                    const auto slope = [](float v, float d) {
-                        const float s = std::is_same<T, float>::value
-                                            ? 1.f / (1.f + expf(-v))
-                                            : rcp_approx(1.f + ex2_approx(-v * kLog2e));
-                        return d * fmaf(v * s, 1.f - s, s);
-                    };
-                    gv = pk2(slope(lo2(v), lo2(dy)), slope(hi2(v), hi2(dy)));
-                }
-                g[q][i] = gv;
-                if (!above) {
-#pragma unroll
-                    for (int k = 0; k < W; ++k)
-                        dw[q][k] = fma2(gv, e[k], dw[q][k]);
-                    db[q] = add2(db[q], gv);
-                }
-            }
-            // the W-1 g behind this block
-            const int src = ((tg + 1) & (ngr - 1)) * (32 / ngr) + cg;
-#pragma unroll
-            for (int k = 0; k < H; ++k) {
-                const uint64_t give = tg == 0 ? head[q][k] : g[q][k];
-                g[q][TB + k] = __shfl_sync(0xffffffffu, (unsigned long long)give, src);
-                head[q][k] = g[q][k];
-            }
-        }
-        if (above)
-            continue;
-        pair_t<T> dp[Q][TB];
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            uint64_t d[TB];
-#pragma unroll
-            for (int i = 0; i < TB; ++i) {
-                uint64_t a = 0;
-#pragma unroll
-                for (int k = 0; k < W; ++k)
-                    a = fma2(w[q][k], g[q][i + H - k], a);
-                d[i] = a;
-            }
-            if (p.dlast && t0 + TB > p.L - H) {
-                // the state that the sequence ends with is its last inputs
-#pragma unroll
-                for (int i = 0; i < TB; ++i) {
-                    const int j = t0 + i - (p.L - H), c = c0 + 2 * q;
-                    if (j >= 0 && j < H) {
-                        const T *dl = static_cast<const T *>(p.dlast) +
-                                      (int64_t(b) * p.dim + c) * H + j;
-                        d[i] = add2(d[i], pk2(c < p.dim ? float(dl[0]) : 0.f,
-                                              c + 1 < p.dim ? float(dl[H]) : 0.f));
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < TB; ++i)
-                dp[q][i] = PairOf<T>::round(d[i]);
-        }
-        if (t0 < p.L)
-            store_block<T, XTOK, CH, TB>(dp, p.dx, b, c0, t0, p.dim, p.L);
-        if (p.dh0 && t0 == 0) {
-            // element j of the initial state is input j - (W-1)
+        if (t0 < p.L) {
+            load_block<T, XTOK, CH, TB, H>(xp, p.x, past, H, b, c0, t0, p.dim, p.L);
+            load_block<T, YTOK, CH, TB, 0>(yp, p.dy, nullptr, 0, b, c0, t0, p.dim, p.L);
+        } else {
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
+#pragma unroll
+                for (int i = 0; i < H + TB; ++i)
+                    xp[q][i] = 0;
+#pragma unroll
+                for (int i = 0; i < TB; ++i)
+                    yp[q][i] = 0;
+            }
+        }
+        const int src = ((tg + 1) & (ngr - 1)) * (32 / ngr) + cg;
+        const bool tail = p.dlast && t0 + TB > p.L - H;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            uint64_t w[W], bias, g[TB + H];
+            taps.read(w, bias, cg * CH + 2 * q);
+            with_flag(p.silu, [&](auto silu) {
+                uint64_t e[W];
+#pragma unroll
+                for (int k = 0; k < H; ++k)
+                    e[k + 1] = PairOf<T>::f2(xp[q][k]);
+#pragma unroll
+                for (int i = 0; i < TB; ++i) {
+#pragma unroll
+                    for (int k = 0; k < H; ++k)
+                        e[k] = e[k + 1];
+                    e[H] = PairOf<T>::f2(xp[q][H + i]);
+                    g[i] = PairOf<T>::f2(yp[q][i]);
+                    if (decltype(silu)::value)
+                        g[i] = silu_grad2<T>(tap_sum<W>(w, e, bias), g[i]);
+                    // (the block above a run adds nothing: see below)
+#pragma unroll
+                    for (int k = 0; k < W; ++k)
+                        dw[q][k] = fma2(g[i], e[k], dw[q][k]);
+                    db[q] = add2(db[q], g[i]);
+                }
+            });
+            // the W-1 g behind this block
+#pragma unroll
+            for (int k = 0; k < H; ++k) {
+                const uint64_t give = tg == 0 ? head[q][k] : g[k];
+                g[TB + k] = __shfl_sync(0xffffffffu, (unsigned long long)give, src);
+                head[q][k] = g[k];
+            }
+            if (p.dh0 && t0 == 0) {
+                // element j of the initial state is input j - (W-1)
 #pragma unroll
                 for (int j = 0; j < H; ++j) {
                     uint64_t a = 0;
 #pragma unroll
                     for (int k = 0; k <= j; ++k)
-                        a = fma2(w[q][k], g[q][j - k], a);
-                    const int c = c0 + 2 * q, o = j - (p.L);  // index in dlast: j - H - (L - H)
-                    float f[2] = {lo2(a), hi2(a)};
+                        a = fma2(w[k], g[j - k], a);
+                    const int c = c0 + 2 * q, o = j - p.L;  // place in dlast, if it is there
+                    const float f[2] = {lo2(a), hi2(a)};
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (c + h >= p.dim)
                             continue;
                         const int64_t row = (int64_t(b) * p.dim + c + h) * H;
-                        if (p.dlast && o >= 0)
-                            f[h] += float(static_cast<const T *>(p.dlast)[row + o]);
-                        static_cast<T *>(p.dh0)[row + j] = T(f[h]);
+                        const float more = p.dlast && o >= 0
+                                               ? float(static_cast<const T *>(p.dlast)[row + o])
+                                               : 0.f;
+                        static_cast<T *>(p.dh0)[row + j] = T(f[h] + more);
                     }
                 }
             }
+#pragma unroll
+            for (int i = 0; i < TB; ++i) {
+                uint64_t a = mul2(w[0], g[i + H]);
+#pragma unroll
+                for (int k = 1; k < W; ++k)
+                    a = fma2(w[k], g[i + H - k], a);
+                g[i] = a;
+            }
+            if (tail) {
+                // the state that the sequence ends with is its last inputs
+                const int c = c0 + 2 * q;
+#pragma unroll
+                for (int i = 0; i < TB; ++i)
+                    if (t0 + i >= p.L - H && t0 + i < p.L) {
+                        const T *dl = static_cast<const T *>(p.dlast) +
+                                      (int64_t(b) * p.dim + c) * H + (t0 + i - (p.L - H));
+                        g[i] = add2(g[i], pk2(c < p.dim ? float(dl[0]) : 0.f,
+                                              c + 1 < p.dim ? float(dl[H]) : 0.f));
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < TB; ++i)
+                yp[q][i] = PairOf<T>::round(g[i]);  // dx, in place of dy
         }
+        if (above) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                db[q] = 0;
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+                    dw[q][k] = 0;
+            }
+        }
+        if (!above && t0 < p.L)
+            store_block<T, XTOK, CH, TB>(yp, p.dx, b, c0, t0, p.dim, p.L);
     }
     // the run's sums over the warp's token blocks
     for (int off = 16; off >= (1 << p.cg_log2); off >>= 1)

@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "selscan.h"
+#include "selscan_debug.h"
 #include "api_common.cuh"
 #include "conv.cuh"
 #include "scan_packed.cuh"
@@ -136,6 +137,59 @@ void launch_conv_bwd(const ConvBwdParams &p, bool xt, bool yt, dim3 grid, cudaSt
     else
         yt ? conv_bwd_kernel<T, W, false, true><<<grid, 128, 0, s>>>(p)
            : conv_bwd_kernel<T, W, false, false><<<grid, 128, 0, s>>>(p);
+}
+
+// Rows of a block of the convolution's single-token kernel: one while the
+// blocks do not fill the GPU several times over, else as many as keep about
+// 1000 blocks (a block's taps are read once for its rows).
+int conv_step_rows(int64_t batch, int64_t gx)
+{
+    const int64_t rows = batch * gx / 1024;
+    return rows < 4 ? (batch * gx <= 1024 ? 1 : 4) : rows >= 16 ? 16 : int(rows / 4 * 4);
+}
+
+int g_dbg_packed_seg = 0;    // test hooks, see selscan_debug_packed_segment
+int g_dbg_packed_lanes = 0;
+
+struct PackedPlan {
+    int lanes;    // per channel
+    int seg_len;  // tokens of a segment
+};
+
+// Lanes per channel and tokens per segment of packed prompts.
+PackedPlan packed_plan(int64_t tokens, int64_t seqs, int64_t dim, int64_t sms)
+{
+    const int64_t warps1 = (dim + 63) / 64, warps4 = 4 * warps1;
+    const auto seg_of = [&](int64_t warps, int64_t slots) {
+        return std::max<int64_t>(64, ((tokens * warps + slots - 1) / slots + 15) / 16 * 16);
+    };
+    const int64_t seg4 = seg_of(warps4, 24 * sms);
+    PackedPlan plan;
+    plan.lanes = g_dbg_packed_lanes ? g_dbg_packed_lanes : (tokens > seqs * seg4 ? 1 : 4);
+    const int64_t seg = plan.lanes == 1 ? seg_of(warps1, 16 * sms) : seg4;
+    plan.seg_len = g_dbg_packed_seg ? g_dbg_packed_seg : int(std::min(seg, kMaxLen));
+    return plan;
+}
+
+template <typename T, int LPC, bool OUT, bool GATE>
+void launch_packed(const ScanPackedParams &p, unsigned grid, cudaStream_t s)
+{
+    constexpr int NT = SpShape<T, LPC>::kThreads;
+    if (p.softplus)
+        scan_packed_kernel<T, LPC, OUT, true, GATE><<<grid, NT, 0, s>>>(p);
+    else
+        scan_packed_kernel<T, LPC, OUT, false, GATE><<<grid, NT, 0, s>>>(p);
+}
+
+template <bool OUT, bool GATE>
+void launch_packed(const ScanPackedParams &p, bool bf, int lanes, unsigned grid, cudaStream_t s)
+{
+    if (lanes == 1)
+        bf ? launch_packed<__nv_bfloat16, 1, OUT, GATE>(p, grid, s)
+           : launch_packed<float, 1, OUT, GATE>(p, grid, s);
+    else
+        bf ? launch_packed<__nv_bfloat16, 4, OUT, GATE>(p, grid, s)
+           : launch_packed<float, 4, OUT, GATE>(p, grid, s);
 }
 
 // f(T tag, integral constant W) for the element type and tap count at hand.
@@ -334,7 +388,7 @@ extern "C" selscan_status selscan_conv_bwd(const selscan_tensor *x, const selsca
     const int ngr = 32 >> p.cg_log2;
     const int64_t tiles = (tblocks + ngr - 1) / ngr;
     // runs: enough warps for every SM, and as few steps above a run as that allows
-    const int64_t want = std::max<int64_t>(1, 16ll * di->sm_count / (int64_t(p.ctiles) * batch));
+    const int64_t want = std::max<int64_t>(1, 32ll * di->sm_count / (int64_t(p.ctiles) * batch));
     int64_t runs = std::min(tiles, want);
     p.steps = int((tiles + runs - 1) / runs);
     runs = (tiles + p.steps - 1) / p.steps;
@@ -348,7 +402,7 @@ extern "C" selscan_status selscan_conv_bwd(const selscan_tensor *x, const selsca
     p.dlast = opt_data(dlast);
     p.dh0 = dh0 ? dh0->data : nullptr;
     p.silu = silu ? 1 : 0;
-    const int64_t gx = (int64_t(p.ctiles) * runs + 3) / 4;
+    const int64_t gx = (runs + 3) / 4 * p.ctiles;
     const int64_t rows = batch * runs;
     if (gx > 0x7fffffffll || rows > 0x7fffffffll || dim * (W + 1) > 0x7fffffffll)
         return SELSCAN_ERR_UNSUPPORTED;
@@ -417,6 +471,7 @@ extern "C" selscan_status selscan_conv_step(selscan_tensor *state, const selscan
         return (dim == 1 || t->stride[1] == 1) && rows_vec(t, es);
     };
     p.vec = dim % blk == 0 && vec_ok(x) && vec_ok(y) && aligned16(state->data);
+    p.wvec = aligned16(weight->data);
     p.batch = int(batch);
     p.dim = int(dim);
     p.x = x->data;
@@ -431,12 +486,18 @@ extern "C" selscan_status selscan_conv_step(selscan_tensor *state, const selscan
     p.slot_count = int(count);
     p.silu = silu ? 1 : 0;
     const int64_t threads = p.vec ? dim / blk : dim;
-    const dim3 grid(unsigned((threads + 127) / 128), unsigned(batch));
+    const int64_t gx = (threads + 127) / 128;
+    p.rows = conv_step_rows(batch, gx);
+    const dim3 grid{unsigned(gx), unsigned((batch + p.rows - 1) / p.rows)};
     dispatch(dt, W, [&](auto tag, auto w) {
         using T = decltype(tag);
         constexpr int WW = decltype(w)::value;
-        p.vec ? conv_step_kernel<T, WW, true><<<grid, 128, 0, stream>>>(p)
-              : conv_step_kernel<T, WW, false><<<grid, 128, 0, stream>>>(p);
+        if (p.vec)
+            p.rows == 1 ? conv_step_kernel<T, WW, true, 1><<<grid, 128, 0, stream>>>(p)
+                        : conv_step_kernel<T, WW, true, 2><<<grid, 128, 0, stream>>>(p);
+        else
+            p.rows == 1 ? conv_step_kernel<T, WW, false, 1><<<grid, 128, 0, stream>>>(p)
+                        : conv_step_kernel<T, WW, false, 2><<<grid, 128, 0, stream>>>(p);
     });
     return counted_launch() == cudaSuccess ? SELSCAN_OK : SELSCAN_ERR_CUDA;
 }
@@ -480,6 +541,7 @@ extern "C" selscan_status selscan_conv_packed(selscan_tensor *state, const selsc
     p.ix.err = di->err;
     const int64_t es = int64_t(elem_size(dt)), blk = 16 / es;
     p.vec = dim % blk == 0 && rows_vec(x, es) && rows_vec(y, es);
+    p.svec = p.vec && aligned16(state->data);
     p.dim = int(dim);
     p.x = x->data;
     p.sx = x->stride[0];
@@ -490,9 +552,9 @@ extern "C" selscan_status selscan_conv_packed(selscan_tensor *state, const selsc
     p.state = state->data;
     p.silu = silu ? 1 : 0;
     p.runs = int((tokens + kConvRun - 1) / kConvRun);
-    const int64_t per = 32 * (p.vec ? blk : 2);
+    const int64_t per = 32 * (p.vec ? blk : 4);
     p.ctiles = int((dim + per - 1) / per);
-    const int64_t blocks = (int64_t(p.runs + 1) * p.ctiles + 3) / 4;
+    const int64_t blocks = (int64_t(p.runs) + 1 + 3) / 4 * p.ctiles;
     if (blocks > 0x7fffffffll)
         return SELSCAN_ERR_UNSUPPORTED;
     dispatch(dt, W, [&](auto tag, auto w) {
@@ -502,6 +564,12 @@ extern "C" selscan_status selscan_conv_packed(selscan_tensor *state, const selsc
               : conv_packed_kernel<T, WW, false><<<unsigned(blocks), 128, 0, stream>>>(p);
     });
     return counted_launch() == cudaSuccess ? SELSCAN_OK : SELSCAN_ERR_CUDA;
+}
+
+extern "C" void selscan_debug_packed_segment(int tokens, int lanes)
+{
+    g_dbg_packed_seg = tokens <= 0 ? 0 : (tokens + 15) / 16 * 16;
+    g_dbg_packed_lanes = lanes == 1 || lanes == 4 ? lanes : 0;
 }
 
 extern "C" selscan_status selscan_fwd_packed(
@@ -555,7 +623,6 @@ extern "C" selscan_status selscan_fwd_packed(
     p.ix.err = di->err;
     const int64_t es = int64_t(elem_size(dt));
     p.dim = int(dim);
-    p.tiles = int((dim + kSpCT - 1) / kSpCT);
     p.vec = rows_vec(u, es) && rows_vec(delta, es) && (!gate || rows_vec(z, es));
     // four bf16 or two fp32 values at a time: 8-byte pieces
     const auto bc_ok = [&](const selscan_tensor *t) {
@@ -581,10 +648,11 @@ extern "C" selscan_status selscan_fwd_packed(
     p.state = static_cast<float *>(state->data);
     p.softplus = delta_softplus ? 1 : 0;
 
-    const int64_t slots_gpu = 4ll * di->sm_count;
-    int64_t seg = (tokens * p.tiles + slots_gpu - 1) / slots_gpu;
-    seg = std::max<int64_t>(64, (seg + 15) / 16 * 16);
-    p.seg_len = int(std::min<int64_t>(seg, kMaxLen));
+    p.y_vec = reinterpret_cast<uintptr_t>(y->data) % uintptr_t(2 * es) == 0 &&
+              (tokens <= 1 || y->stride[0] % 2 == 0);
+    const PackedPlan plan = packed_plan(tokens, p.ix.seqs, dim, di->sm_count);
+    p.tiles = int((dim + 63) / 64);
+    p.seg_len = plan.seg_len;
     const int64_t units = tokens / p.seg_len + p.ix.seqs;
     if (units * p.tiles > 0x7fffffffll)
         return SELSCAN_ERR_UNSUPPORTED;
@@ -598,10 +666,7 @@ extern "C" selscan_status selscan_fwd_packed(
             return SELSCAN_ERR_CUDA;
         p.agg = static_cast<float *>(ws);
         p.agg_sd = p.agg + entries * size_t(dim) * kDiagN;
-        if (bf)
-            scan_packed_kernel<__nv_bfloat16, false><<<grid, kSpCT, 0, stream>>>(p);
-        else
-            scan_packed_kernel<float, false><<<grid, kSpCT, 0, stream>>>(p);
+        launch_packed<false, false>(p, bf, plan.lanes, grid, stream);
         le = counted_launch();
         if (le == cudaSuccess) {
             const dim3 fg{unsigned((dim * kDiagN + 255) / 256), unsigned(p.ix.seqs)};
@@ -610,10 +675,8 @@ extern "C" selscan_status selscan_fwd_packed(
         }
     }
     if (le == cudaSuccess) {
-        if (bf)
-            scan_packed_kernel<__nv_bfloat16, true><<<grid, kSpCT, 0, stream>>>(p);
-        else
-            scan_packed_kernel<float, true><<<grid, kSpCT, 0, stream>>>(p);
+        gate ? launch_packed<true, true>(p, bf, plan.lanes, grid, stream)
+             : launch_packed<true, false>(p, bf, plan.lanes, grid, stream);
         le = counted_launch();
     }
     if (ws)

@@ -11,7 +11,7 @@
 // yet), which is left as the state after the sequence's last token.
 //
 // Work split.  A unit is a segment of at most seg_len tokens of one sequence
-// times 128 channels, one thread per channel with its 16 states in registers.
+// times kSpCT channels, one thread per channel with its 16 states in registers.
 // The lengths are on the device, so the grid holds an upper bound of units,
 // tokens / seg_len + seqs, and a block finds its sequence by searching the
 // map i -> start[i] / seg_len + i, whose steps leave room for every
@@ -37,7 +37,9 @@ namespace selscan {
 struct ScanPackedParams {
     PackedIndex ix;
     int dim, seg_len, tiles;
-    int vec, bc_vec;    // whole 16-byte (8-byte for B, C) pieces may be read
+    int vec;            // whole 16-byte pieces of rows may be read
+    int y_vec;          // pairs of channels may be written as one word
+    int bc_vec;         // whole pieces of four values of B and C may be read
     const void *u, *delta, *z, *B, *C;
     int64_t su, sd, sz, sB, sC;  // row strides
     void *y;
@@ -49,8 +51,6 @@ struct ScanPackedParams {
     float *agg_sd; // [2 (tokens / seg_len) + 2][dim]
 };
 
-constexpr int kSpCT = 128;  // channels of a unit
-
 // First entry of a sequence's segments in agg: a sequence of two segments or
 // more crosses at least half as many multiples of seg_len.
 __device__ __forceinline__ int64_t packed_agg(int begin, int seg_len)
@@ -58,86 +58,274 @@ __device__ __forceinline__ int64_t packed_agg(int begin, int seg_len)
     return 2 * int64_t(begin / seg_len);
 }
 
-template <typename T>
-__device__ __forceinline__ float packed_step(float raw, int softplus)
+// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) <= 1, with log1p(e) = 2
+// atanh(e / (2 + e)): an odd series in s = e / (2 + e) <= 1/3, so that small
+// step sizes keep their relative accuracy (about 5e-7 with the fast e and
+// reciprocal; lg2 of 1 + e would lose 1.5e-5 where e is 2^-6).  The
+// coefficients are a least-maximum fit of 2 atanh(s) / s in s^2 (relative
+// error 4e-9).
+__device__ __forceinline__ uint64_t packed_softplus(uint64_t x)
 {
-    if (!softplus)
-        return raw;
-    return std::is_same<T, float>::value ? softplus_exact(raw) : softplus_fast(raw);
+    const auto k = [](float v) { return pk2(v, v); };
+    const uint64_t m = mul2(pk2(-fabsf(lo2(x)), -fabsf(hi2(x))), k(kLog2e));
+    const uint64_t e = pk2(ex2_approx(lo2(m)), ex2_approx(hi2(m)));
+    const uint64_t d = add2(e, k(2.f));
+    const uint64_t s = mul2(e, pk2(rcp_approx(lo2(d)), rcp_approx(hi2(d)))), w = mul2(s, s);
+    uint64_t q = k(0.2817833423614502f);
+    q = fma2(q, w, k(0.27960601449012756f));
+    q = fma2(q, w, k(0.40024909377098083f));
+    q = fma2(q, w, k(0.6666631698608398f));
+    q = fma2(q, w, k(2.0f));
+    return fma2(s, q, pk2(fmaxf(lo2(x), 0.f), fmaxf(hi2(x), 0.f)));
 }
 
-template <typename T>
+// 2^x of a pair in fp32: x = n + f with n the nearest integer, 2^f = 1 + f
+// p(f) (a least-maximum fit on |f| <= 1/2, relative error 3e-9 before rounding,
+// whose first coefficient is ln 2, so that factors next to 1, whose products
+// run over thousands of tokens, are not biased), 2^n added to the exponent.
+// x is held to [-125, 127].
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t x)
+{
+    constexpr float kRound = 12582912.f;  // 1.5 * 2^23: integers in the low bits
+    const uint64_t c = pk2(fminf(fmaxf(lo2(x), -125.f), 127.f), fminf(fmaxf(hi2(x), -125.f), 127.f));
+    const uint64_t t = add2(c, pk2(kRound, kRound));
+    const uint64_t f = add2(c, fma2(t, pk2(-1.f, -1.f), pk2(kRound, kRound)));
+    uint64_t q;
+    const auto k = [](float v) { return pk2(v, v); };
+    q = k(0.00015324314881581813f);
+    q = fma2(q, f, k(0.0013390958774834871f));
+    q = fma2(q, f, k(0.009618517942726612f));
+    q = fma2(q, f, k(0.05550359562039375f));
+    q = fma2(q, f, k(0.24022647738456726f));
+    q = fma2(q, f, k(kLn2));
+    q = fma2(q, f, k(1.f));
+    const auto scale = [](float v, float n) {
+        return __uint_as_float(__float_as_uint(v) + (__float_as_uint(n) << 23));
+    };
+    return pk2(scale(lo2(q), lo2(t)), scale(hi2(q), hi2(t)));
+}
+
+// Shape of a unit.  A thread holds two adjacent channels (one row of B and C
+// from shared memory serves both: at one channel per thread those broadcast
+// loads, 128 bytes per channel and token, would bound the kernel), and LPC
+// lanes share them, 16 / LPC states each:
+//  1: least work per token (the powers of the POW form are one running
+//     product);
+//  2, 4: a token takes a half, a quarter of the time, so that sequences need
+//     not be cut into segments to fill the GPU.  Of four tokens the lanes
+//     prepare two or one each (step sizes, gate) and exchange.
+template <typename T, int LPC>
 struct SpShape {
-    static constexpr int kTC = std::is_same<T, float>::value ? 8 : 16;  // tokens staged at once
+    static constexpr int kCT = 64;  // channels
+    static constexpr int kThreads = kCT / 2 * LPC;
+    static constexpr int kTC = 32 / int(sizeof(T));  // tokens staged at once
+    // row pitch: with LPC lanes per channel a warp reads LPC rows at once;
+    // 128 / LPC bytes more put them into different banks
+    static constexpr int kPitch = kCT + (LPC == 1 ? 0 : 128 / LPC / int(sizeof(T)));
+    static constexpr int kBlocks = LPC == 1 ? 12 : LPC == 2 ? 8 : 6;  // resident per SM
 };
 
-// One chunk of n tokens for one channel.  OUT: also the outputs.
-// POW: A[n] = (n+1) A[0], so that the 16 decays are powers of one.
-template <typename T, bool OUT, bool POW>
-__device__ __forceinline__ void packed_chunk(uint64_t (&h)[8], float &sum, int n, const T *us,
-                                             const T *ds, const T *zs, const float *bc,
-                                             const uint64_t (&a2)[8], float a0, float bias,
-                                             float dskip, int softplus, bool gate, T *y,
-                                             int64_t sy, bool live)
+// What a thread holds of its two channels.
+template <int LPC>
+struct SpChannels {
+    static constexpr int Q = 8 / LPC;  // pairs of states
+    uint64_t h[2][Q], a2[2][Q];        // the states; A times log2 e
+    uint64_t a0, bias, dskip, sum;     // of both channels
+    int j;                             // lane of the channels
+    int chans;                         // how many of the two exist
+    bool pair;                         // both, and y takes them as one word
+};
+
+// The decays exp(delta A[n]) of one token of channel ch.  POW: A[n] = (n+1)
+// A[0] (bf16), so that they are powers of one exponential.
+template <typename T, int LPC, bool POW>
+__device__ __forceinline__ void packed_decay(uint64_t (&e)[8 / LPC], const SpChannels<LPC> &s,
+                                             int ch, float dt)
 {
     constexpr bool kFast = !std::is_same<T, float>::value;
-#pragma unroll 4
-    for (int t = 0; t < n; ++t) {
-        const float u = float(us[t * kSpCT]);
-        const float dt = packed_step<T>(float(ds[t * kSpCT]) + bias, softplus);
-        const float dx = dt * u;
-        const uint64_t dx2 = pk2(dx, dx), dt2 = pk2(dt, dt);
-        uint64_t e[8];
-        if (POW && kFast) {
-            const float r = ex2_approx(dt * a0), r2 = r * r;
-            const uint64_t rr = pk2(r2, r2);
+    constexpr int Q = 8 / LPC;
+    if (POW) {
+        const float r = ex2_approx(dt * (ch ? hi2(s.a0) : lo2(s.a0))), r2 = r * r;
+        const uint64_t rr = pk2(r2, r2);
+        if (LPC == 1) {
             e[0] = pk2(r, r2);
-#pragma unroll
-            for (int k = 1; k < 8; ++k)
-                e[k] = mul2(e[k - 1], rr);
         } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint64_t x = mul2(dt2, a2[k]);
-                e[k] = kFast ? pk2(ex2_approx(lo2(x)), ex2_approx(hi2(x)))
-                             : pk2(exp_decay(lo2(x)), exp_decay(hi2(x)));
-            }
+            // r^(16 j / LPC + 1) from A itself
+            const float f = ex2_approx(dt * lo2(s.a2[ch][0]));
+            e[0] = pk2(f, f * r);
         }
-        const ulonglong2 *row = reinterpret_cast<const ulonglong2 *>(bc + t * 32);
-        uint64_t acc0 = 0, acc1 = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const ulonglong2 B = row[k];
-            h[2 * k] = fma2(e[2 * k], h[2 * k], mul2(dx2, B.x));
-            h[2 * k + 1] = fma2(e[2 * k + 1], h[2 * k + 1], mul2(dx2, B.y));
+        for (int k = 1; k < Q; ++k)
+            e[k] = mul2(e[k - 1], rr);
+        return;
+    }
+    const uint64_t dt2 = pk2(dt, dt);
+#pragma unroll
+    for (int k = 0; k < Q; ++k) {
+        const uint64_t x = mul2(dt2, s.a2[ch][k]);
+        e[k] = kFast ? pk2(ex2_approx(lo2(x)), ex2_approx(hi2(x))) : exp2_pair(x);
+    }
+}
+
+// Two channels' staged values of one token.
+__device__ __forceinline__ uint64_t packed_two(const __nv_bfloat16 *p)
+{
+    return bf2_to_f2(*reinterpret_cast<const uint32_t *>(p));
+}
+__device__ __forceinline__ uint64_t packed_two(const float *p)
+{
+    const float2 v = *reinterpret_cast<const float2 *>(p);
+    return pk2(v.x, v.y);
+}
+
+// Step size and step size times input of the tokens that this lane prepares.
+template <int OWN>
+struct SpPrep {
+    uint64_t dt[OWN], dx[OWN];
+};
+
+template <typename T, int LPC, bool SOFT, bool FULL>
+__device__ __forceinline__ SpPrep<4 / LPC> packed_prepare(const SpChannels<LPC> &s, int t0, int n,
+                                                          const T *us, const T *ds)
+{
+    constexpr bool kFast = !std::is_same<T, float>::value;
+    constexpr int P = SpShape<T, LPC>::kPitch, OWN = 4 / LPC;
+    SpPrep<OWN> r;
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+        const int t = t0 + i * LPC + s.j;
+        uint64_t d = add2(packed_two(ds + t * P), s.bias);
+        if (SOFT)
+            d = kFast ? packed_softplus(d) : pk2(softplus_exact(lo2(d)), softplus_exact(hi2(d)));
+        const uint64_t x = mul2(d, packed_two(us + t * P));
+        // tokens from n on get a zero step, which leaves the state as it is
+        r.dt[i] = FULL || t < n ? d : 0;
+        r.dx[i] = FULL || t < n ? x : 0;
+    }
+    return r;
+}
+
+// One token's outputs of channels c and c + 1, of which `chans` exist.
+__device__ __forceinline__ void packed_store(__nv_bfloat16 *y, uint64_t v, int chans, bool pair)
+{
+    if (pair)
+        *reinterpret_cast<uint32_t *>(y) = pack2_bf16(lo2(v), hi2(v));
+    else {
+        if (chans > 0)
+            y[0] = __float2bfloat16_rn(lo2(v));
+        if (chans > 1)
+            y[1] = __float2bfloat16_rn(hi2(v));
+    }
+}
+__device__ __forceinline__ void packed_store(float *y, uint64_t v, int chans, bool pair)
+{
+    if (pair)
+        *reinterpret_cast<float2 *>(y) = make_float2(lo2(v), hi2(v));
+    else {
+        if (chans > 0)
+            y[0] = lo2(v);
+        if (chans > 1)
+            y[1] = hi2(v);
+    }
+}
+
+// n tokens (staged at us, ds, zs; B and C rows at bc) of two channels, four at
+// a time; the next four's step sizes are prepared meanwhile.  FULL: n is the
+// whole chunk.
+template <typename T, int LPC, bool OUT, bool POW, bool SOFT, bool GATE, bool FULL>
+__device__ __forceinline__ void packed_chunk(SpChannels<LPC> &s, int n, const T *us, const T *ds,
+                                             const T *zs, const float *bc, T *y, int64_t sy)
+{
+    constexpr int P = SpShape<T, LPC>::kPitch, TC = SpShape<T, LPC>::kTC, Q = 8 / LPC;
+    constexpr int OWN = 4 / LPC;  // tokens of four that this lane prepares
+    SpPrep<OWN> cur = packed_prepare<T, LPC, SOFT, FULL>(s, 0, n, us, ds);
+#pragma unroll 1
+    for (int t0 = 0; t0 < (FULL ? TC : n); t0 += 4) {
+        const SpPrep<OWN> next =
+            packed_prepare<T, LPC, SOFT, FULL>(s, min(t0 + 4, TC - 4), n, us, ds);
+        uint64_t part[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint64_t d = cur.dt[i / LPC], x = cur.dx[i / LPC];
+            if (LPC > 1) {
+                const int from = (threadIdx.x & (32 - LPC)) + i % LPC;
+                d = pk2(__shfl_sync(0xffffffffu, lo2(d), from), __shfl_sync(0xffffffffu, hi2(d), from));
+                x = pk2(__shfl_sync(0xffffffffu, lo2(x), from), __shfl_sync(0xffffffffu, hi2(x), from));
+            } else if (!OUT) {
+                s.sum = add2(s.sum, d);
+            }
+            uint64_t e[2][Q], acc[2][2];
+            packed_decay<T, LPC, POW>(e[0], s, 0, lo2(d));
+            packed_decay<T, LPC, POW>(e[1], s, 1, hi2(d));
+            const uint64_t x2[2] = {pk2(lo2(x), lo2(x)), pk2(hi2(x), hi2(x))};
+            const ulonglong2 *row = reinterpret_cast<const ulonglong2 *>(bc + (t0 + i) * 32);
+#pragma unroll
+            for (int k = 0; k < Q / 2; ++k) {
+                const ulonglong2 B = row[k];
+                const ulonglong2 C = OUT ? row[4 + k] : B;
+#pragma unroll
+                for (int ch = 0; ch < 2; ++ch) {
+                    uint64_t(&h)[Q] = s.h[ch];
+                    h[2 * k] = fma2(e[ch][2 * k], h[2 * k], mul2(x2[ch], B.x));
+                    h[2 * k + 1] = fma2(e[ch][2 * k + 1], h[2 * k + 1], mul2(x2[ch], B.y));
+                    if (OUT) {
+                        acc[ch][0] = k ? fma2(C.x, h[2 * k], acc[ch][0]) : mul2(C.x, h[0]);
+                        acc[ch][1] = k ? fma2(C.y, h[2 * k + 1], acc[ch][1]) : mul2(C.y, h[1]);
+                    }
+                }
+            }
             if (OUT) {
-                const ulonglong2 C = row[4 + k];
-                acc0 = fma2(C.x, h[2 * k], acc0);
-                acc1 = fma2(C.y, h[2 * k + 1], acc1);
+                const uint64_t a = add2(acc[0][0], acc[0][1]), b = add2(acc[1][0], acc[1][1]);
+                part[i] = add2(pk2(lo2(a), lo2(b)), pk2(hi2(a), hi2(b)));
             }
         }
-        if (OUT) {
-            const uint64_t acc = add2(acc0, acc1);
-            float v = fmaf(dskip, u, lo2(acc) + hi2(acc));
-            if (gate) {
-                const float zv = float(zs[t * kSpCT]);
-                v *= kFast ? silu_fast(zv) : silu_exact(zv);
+        if (LPC > 1 && !OUT)
+#pragma unroll
+            for (int i = 0; i < OWN; ++i)
+                s.sum = add2(s.sum, cur.dt[i]);
+        cur = next;
+        if (!OUT)
+            continue;
+        if (LPC > 1) {
+            // the sums of its own tokens come to each lane
+            const auto swap = [](uint64_t v, int lanes) {
+                return uint64_t(__shfl_xor_sync(0xffffffffu, (unsigned long long)v, lanes));
+            };
+            const bool up = s.j & 2, odd = s.j & 1;
+            if (LPC == 4) {
+                part[0] = add2(up ? part[2] : part[0], swap(up ? part[0] : part[2], 2));
+                part[1] = add2(up ? part[3] : part[1], swap(up ? part[1] : part[3], 2));
             }
-            if (live)
-                y[t * sy] = T(v);
-        } else {
-            sum += dt;
+#pragma unroll
+            for (int i = 0; i < OWN; ++i)
+                part[i] = add2(odd ? part[2 * i + 1] : part[2 * i],
+                               swap(odd ? part[2 * i] : part[2 * i + 1], 1));
+        }
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            const int t = t0 + i * LPC + s.j;
+            uint64_t v = fma2(s.dskip, packed_two(us + t * P), part[i]);
+            if (GATE) {
+                const uint64_t z = packed_two(zs + t * P);
+                v = mul2(v, silu2<T>(z));
+            }
+            if (FULL || t < n)
+                packed_store(y + t * sy, v, s.chans, s.pair);
         }
     }
 }
 
 // OUT false: the first pass of sequences with several segments.
-template <typename T, bool OUT>
-__global__ void __launch_bounds__(kSpCT) scan_packed_kernel(const __grid_constant__ ScanPackedParams p)
+template <typename T, int LPC, bool OUT, bool SOFT, bool GATE>
+__global__ void __launch_bounds__(SpShape<T, LPC>::kThreads, SpShape<T, LPC>::kBlocks)
+    scan_packed_kernel(const __grid_constant__ ScanPackedParams p)
 {
-    constexpr int TC = SpShape<T>::kTC, VEC = 16 / int(sizeof(T));
+    using Shape = SpShape<T, LPC>;
+    constexpr int TC = Shape::kTC, VEC = 16 / int(sizeof(T));
+    constexpr int CT = Shape::kCT, NT = Shape::kThreads, Q = 8 / LPC;
+    constexpr int NS = GATE ? 3 : 2;  // staged rows: u (later y), Delta, z
     constexpr bool kFast = !std::is_same<T, float>::value;
-    __shared__ __align__(16) T tile[2][OUT ? 3 : 2][TC][kSpCT];
+    __shared__ __align__(16) T tile[2][NS][TC][Shape::kPitch];
     __shared__ __align__(16) float bcf[2][TC][32];
     const PackedIndex &ix = p.ix;
     const int tid = threadIdx.x, lane = tid & 31;
@@ -151,20 +339,23 @@ __global__ void __launch_bounds__(kSpCT) scan_packed_kernel(const __grid_constan
         if (ix.slots[unit] >= 0 && (bg < 0 || en < bg || en > ix.tokens))
             atomicOr(ix.err, kErrIndex);
     }
-    const int s = packed_find(ix, unit, p.seg_len, 1, lane);
+    const PackedView view(ix, lane);
+    const int sq = view.find(unit, p.seg_len, 1);
     PackedSeq q;
-    if (!packed_seq(ix, s, lane, q))
+    if (!view.get(sq, q))
         return;
-    const int64_t seg = unit - (int64_t(q.begin) / p.seg_len + s);
+    const int64_t seg = unit - (int64_t(q.begin) / p.seg_len + sq);
     const int len = q.end - q.begin;
     const int64_t lo = seg * p.seg_len;
-    const int cbase = ct * kSpCT, c = cbase + tid;
-    const bool live = c < p.dim;
-    float *st = p.state + (int64_t(q.slot) * p.dim + (live ? c : 0)) * kDiagN;
+    const int cbase = ct * CT, c = cbase + tid / LPC * 2, j = tid % LPC;  // channels c, c + 1
+    const int chans = min(2, max(0, p.dim - c));
+    const int n0 = j * (kDiagN / LPC);  // this lane's first state
+    float *st = p.state + (int64_t(q.slot) * p.dim + (chans ? c : 0)) * kDiagN + n0;
     if (seg < 0 || lo >= len) {
-        if (OUT && len == 0 && seg == 0 && q.fresh && live)
-            for (int k = 0; k < kDiagN; ++k)
-                st[k] = 0.f;
+        if (OUT && len == 0 && seg == 0 && q.fresh)
+            for (int ch = 0; ch < chans; ++ch)
+                for (int k = 0; k < kDiagN / LPC; ++k)
+                    st[ch * kDiagN + k] = 0.f;
         return;
     }
     const bool many = len > p.seg_len;
@@ -173,143 +364,166 @@ __global__ void __launch_bounds__(kSpCT) scan_packed_kernel(const __grid_constan
     if (!OUT && (!many || last))
         return;
     const int64_t ag = packed_agg(q.begin, p.seg_len) + seg;
-    float *agg = p.agg + (ag * p.dim + (live ? c : 0)) * kDiagN;
-
-    uint64_t h[8], a2[8];
-    float a0 = 0.f, bias = 0.f, dskip = 0.f;
-    bool pow = true;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        h[k] = a2[k] = 0;
-    if (live) {
-        const float scale = kFast ? kLog2e : 1.f;
-        const float2 *ar = reinterpret_cast<const float2 *>(p.A + int64_t(c) * kDiagN);
-        const float first = p.A[int64_t(c) * kDiagN];
-        a0 = first * scale;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float2 a = ar[k];
-            pow = pow && a.x == float(2 * k + 1) * first && a.y == float(2 * k + 2) * first;
-            a2[k] = pk2(a.x * scale, a.y * scale);
-        }
-        if (p.delta_bias)
-            bias = p.delta_bias[c];
-        if (p.Dskip)
-            dskip = p.Dskip[c];
-        if (OUT && (many || !q.fresh)) {
-            const float2 *src = reinterpret_cast<const float2 *>(many ? agg : st);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float2 v = src[k];
-                h[k] = pk2(v.x, v.y);
-            }
-        }
-    }
-    pow = __all_sync(0xffffffffu, pow);
+    float *agg = p.agg + (ag * p.dim + (chans ? c : 0)) * kDiagN + n0;
 
     const int t_first = q.begin + int(lo);
     const int chunks = (n_all + TC - 1) / TC;
     const T *src[3] = {static_cast<const T *>(p.u), static_cast<const T *>(p.delta),
                        static_cast<const T *>(p.z)};
     const int64_t stride[3] = {p.su, p.sd, p.sz};
-    const bool gate = OUT && p.z;
-    const int streams = gate ? 3 : 2;
+    constexpr int PR = CT / VEC;  // 16-byte pieces of a row
 
     // rows of a chunk into shared memory: 16-byte pieces, cut at the last
     // channel and zero-filled behind it
-    const auto fetch = [&](int k) {
+    const int pr = tid / PR, po = (tid % PR) * VEC;
+    const int have = min(VEC, max(0, p.dim - cbase - po));
+    const T *at[NS];
+#pragma unroll
+    for (int v = 0; v < NS; ++v)
+        at[v] = src[v] + (have ? (int64_t(t_first) + pr) * stride[v] + cbase + po : 0);
+    const auto fetch = [&](int k, int buf) {
         const int n = min(TC, n_all - k * TC);
-        const int64_t t0 = t_first + int64_t(k) * TC;
-        for (int v = 0; v < streams; ++v) {
-            const T *b = src[v] + cbase;
-            T(*dst)[kSpCT] = tile[k & 1][v];
+        constexpr int STEP = NT / PR;  // rows between a thread's pieces
+#pragma unroll
+        for (int v = 0; v < NS; ++v) {
             if (p.vec) {
-                constexpr int PR = kSpCT / VEC;  // pieces per row
-                for (int i = tid; i < n * PR; i += kSpCT) {
-                    const int r = i / PR, o = (i % PR) * VEC;
-                    const int have = min(VEC, max(0, p.dim - cbase - o));
-                    cp_async16(&dst[r][o], have ? b + (t0 + r) * stride[v] + o : src[v],
-                               uint32_t(have) * uint32_t(sizeof(T)));
+                const T *g = at[v];
+#pragma unroll
+                for (int i = 0; i < (TC + STEP - 1) / STEP; ++i) {
+                    if (pr + i * STEP < n)
+                        cp_async16(&tile[buf][v][pr + i * STEP][po], g,
+                                   uint32_t(have) * uint32_t(sizeof(T)));
+                    g += have ? STEP * stride[v] : 0;
                 }
+                at[v] += have ? TC * stride[v] : 0;
             } else {
-                for (int r = 0; r < n; ++r)
-                    dst[r][tid] = live ? b[(t0 + r) * stride[v] + tid] : T(0.f);
+                const T *b = src[v] + (t_first + int64_t(k) * TC) * stride[v] + cbase;
+                for (int i = tid; i < n * CT; i += NT) {
+                    const int r = i / CT, o = i % CT;
+                    tile[buf][v][r][o] = cbase + o < p.dim ? b[r * stride[v] + o] : T(0.f);
+                }
             }
         }
         cp_async_commit();
     };
-    // B and C of a chunk: 4 values per thread and 16 tokens
-    constexpr int BV = TC * 32 / kSpCT;  // values per thread
-    float bcv[BV];
+    // B and C of a chunk: loaded a chunk ahead as they are, widened to fp32
+    // when they are stored
+    constexpr int BV = 4, BN = (TC * 32 / BV + NT - 1) / NT;  // values per load, loads
+    pair_t<T> bcw[BN][BV / 2];
     const auto bc_load = [&](int k) {
-        const int r = tid * BV / 32, o = tid * BV % 32;
-        const int t = k * TC + r;
-        const T *m = static_cast<const T *>(o < 16 ? p.B : p.C) +
-                     (int64_t(t_first) + t) * (o < 16 ? p.sB : p.sC) + (o & 15);
-        if (t >= n_all || (!OUT && o >= 16)) {
 #pragma unroll
-            for (int i = 0; i < BV; ++i)
-                bcv[i] = 0.f;
-        } else if (p.bc_vec) {
-            pair_t<T> w[BV / 2];
-            load_row<T, BV>(m, w);
-#pragma unroll
-            for (int i = 0; i < BV / 2; ++i) {
-                const uint64_t f = PairOf<T>::f2(w[i]);
-                bcv[2 * i] = lo2(f);
-                bcv[2 * i + 1] = hi2(f);
+        for (int l = 0; l < BN; ++l) {
+            const int i = (l * NT + tid) * BV, r = i / 32, o = i % 32;
+            const int t = k * TC + r;
+            const T *m = static_cast<const T *>(o < 16 ? p.B : p.C) +
+                         (int64_t(t_first) + t) * (o < 16 ? p.sB : p.sC) + (o & 15);
+            if (r >= TC || t >= n_all || (!OUT && o >= 16)) {
+                bcw[l][0] = bcw[l][1] = 0;
+            } else if (p.bc_vec) {
+                load_row<T, BV>(m, bcw[l]);
+            } else {
+                bcw[l][0] = PairOf<T>::make(m[0], m[1]);
+                bcw[l][1] = PairOf<T>::make(m[2], m[3]);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < BV; ++i)
-                bcv[i] = float(m[i]);
         }
     };
     const auto bc_put = [&](int k) {
-        float *d = &bcf[k & 1][0][0] + tid * BV;
 #pragma unroll
-        for (int i = 0; i < BV; ++i)
-            d[i] = bcv[i];
-    };
-
-    float sum = 0.f;
-    fetch(0);
-    bc_load(0);
-    bc_put(0);
-    for (int k = 0; k < chunks; ++k) {
-        if (k + 1 < chunks) {
-            fetch(k + 1);
-            bc_load(k + 1);
-            cp_async_wait<1>();
-        } else {
-            cp_async_wait<0>();
+        for (int l = 0; l < BN; ++l) {
+            const uint64_t a = PairOf<T>::f2(bcw[l][0]), c2 = PairOf<T>::f2(bcw[l][1]);
+            if ((l * NT + tid) * BV < TC * 32)
+                *reinterpret_cast<float4 *>(&bcf[k & 1][0][0] + (l * NT + tid) * BV) =
+                    make_float4(lo2(a), hi2(a), lo2(c2), hi2(c2));
         }
-        __syncthreads();
+    };
+    fetch(0, 0);
+    bc_load(0);
+
+    SpChannels<LPC> s;
+    s.j = j;
+    s.chans = chans;
+    s.pair = chans == 2 && p.y_vec;
+    bool pow = kFast;
+    {
+        float a0[2] = {0.f, 0.f}, bias[2] = {0.f, 0.f}, dskip[2] = {0.f, 0.f};
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+#pragma unroll
+            for (int k = 0; k < Q; ++k)
+                s.h[ch][k] = s.a2[ch][k] = 0;
+            if (ch >= chans)
+                continue;
+            const float *ar = p.A + int64_t(c + ch) * kDiagN;
+            const float first = ar[0];
+            a0[ch] = first * kLog2e;
+#pragma unroll
+            for (int k = 0; k < Q; ++k) {
+                const float2 a = *reinterpret_cast<const float2 *>(ar + n0 + 2 * k);
+                pow = pow && a.x == float(n0 + 2 * k + 1) * first &&
+                      a.y == float(n0 + 2 * k + 2) * first;
+                s.a2[ch][k] = pk2(a.x * kLog2e, a.y * kLog2e);
+            }
+            if (p.delta_bias)
+                bias[ch] = p.delta_bias[c + ch];
+            if (p.Dskip)
+                dskip[ch] = p.Dskip[c + ch];
+            if (OUT && (many || !q.fresh)) {
+                const float *from = (many ? agg : st) + ch * kDiagN;
+#pragma unroll
+                for (int k = 0; k < Q; ++k) {
+                    const float2 v = *reinterpret_cast<const float2 *>(from + 2 * k);
+                    s.h[ch][k] = pk2(v.x, v.y);
+                }
+            }
+        }
+        s.a0 = pk2(a0[0], a0[1]);
+        s.bias = pk2(bias[0], bias[1]);
+        s.dskip = pk2(dskip[0], dskip[1]);
+        s.sum = 0;
+    }
+    pow = __all_sync(0xffffffffu, pow);
+    bc_put(0);
+
+    for (int k = 0; k < chunks; ++k) {
+        const int buf = k & 1;
+        cp_async_wait<0>();
+        __syncthreads();  // chunk k is there; chunk k - 1 is done
+        if (k + 1 < chunks) {
+            fetch(k + 1, buf ^ 1);
+            bc_load(k + 1);
+        }
         const int n = min(TC, n_all - k * TC);
-        T *y = static_cast<T *>(p.y) + (t_first + int64_t(k) * TC) * p.sy + c;
-        const T *us = &tile[k & 1][0][0][tid], *ds = &tile[k & 1][1][0][tid];
-        const T *zs = &tile[k & 1][OUT ? 2 : 0][0][tid];
-        const float *bc = &bcf[k & 1][0][0];
-        if (pow)
-            packed_chunk<T, OUT, true>(h, sum, n, us, ds, zs, bc, a2, a0, bias, dskip, p.softplus,
-                                       gate, y, p.sy, live);
+        const T *us = &tile[buf][0][0][tid / LPC * 2];
+        const T *ds = &tile[buf][1][0][tid / LPC * 2], *zs = &tile[buf][NS - 1][0][tid / LPC * 2];
+        const float *bc = &bcf[buf][0][n0];
+        T *y = OUT ? static_cast<T *>(p.y) + (t_first + int64_t(k) * TC) * p.sy + c : nullptr;
+        if (kFast && pow && n == TC)
+            packed_chunk<T, LPC, OUT, kFast, SOFT, GATE, kFast>(s, n, us, ds, zs, bc, y, p.sy);
+        else if (n == TC)
+            packed_chunk<T, LPC, OUT, false, SOFT, GATE, true>(s, n, us, ds, zs, bc, y, p.sy);
         else
-            packed_chunk<T, OUT, false>(h, sum, n, us, ds, zs, bc, a2, a0, bias, dskip,
-                                        p.softplus, gate, y, p.sy, live);
+            packed_chunk<T, LPC, OUT, false, SOFT, GATE, false>(s, n, us, ds, zs, bc, y, p.sy);
         if (k + 1 < chunks)
             bc_put(k + 1);
-        __syncthreads();
     }
-    if (!live)
-        return;
     if (OUT && !last)
         return;
-    float2 *dst = reinterpret_cast<float2 *>(OUT ? st : agg);
+    float sum[2] = {lo2(s.sum), hi2(s.sum)};
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-        dst[k] = make_float2(lo2(h[k]), hi2(h[k]));
-    if (!OUT)
-        p.agg_sd[ag * p.dim + c] = sum;
+    for (int ch = 0; ch < 2; ++ch) {
+        if (!OUT)
+#pragma unroll
+            for (int o = 1; o < LPC; o *= 2)
+                sum[ch] += __shfl_xor_sync(0xffffffffu, sum[ch], o);
+        if (ch >= chans)
+            continue;
+        float *dst = (OUT ? st : agg) + ch * kDiagN;
+#pragma unroll
+        for (int k = 0; k < Q; ++k)
+            *reinterpret_cast<float2 *>(dst + 2 * k) = make_float2(lo2(s.h[ch][k]), hi2(s.h[ch][k]));
+        if (!OUT && j == 0)
+            p.agg_sd[ag * p.dim + c + ch] = sum[ch];
+    }
 }
 
 // The start state of every segment of the sequences that have several, in
@@ -323,7 +537,8 @@ static __global__ void __launch_bounds__(256) scan_packed_fold_kernel(const __gr
     if (int64_t(end) - begin <= p.seg_len)
         return;
     PackedSeq q;
-    if (!packed_seq(ix, s, threadIdx.x & 31, q) || i >= p.dim * kDiagN)
+    const PackedView view(ix, threadIdx.x & 31);
+    if (!view.get(s, q) || i >= p.dim * kDiagN)
         return;
     const int c = i / kDiagN;
     const float a = p.A[i];

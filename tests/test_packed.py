@@ -130,6 +130,51 @@ def test_scan_packed_matches_plain(dtype, D):
                 assert rel(got[rows], y_ref[rows]) <= (1e-5 if dtype == "f32" else 5e-3), (lens, i)
 
 
+@pytest.mark.parametrize("lanes", [1, 4])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_scan_packed_forms(lanes, dtype):
+    """Both splits of a channel's states over lanes, in segments of 16 to 48
+    tokens, with A of every kind: powers, general, partly positive, wide
+    (decays that underflow)."""
+    import selective_state_space_selscan_b200 as ss
+    rng = np.random.default_rng(33)
+    D = 136
+    try:
+        for j, (seg, lens) in enumerate([(16, [100, 3, 33]), (32, [64, 0, 65, 1]), (48, [200]),
+                                         (0, [37, 5])]):
+            ss.debug_packed_segment(seg, lanes)
+            for kind in ("real", "free", "positive", "wide"):
+                pk = Packed(rng, lens, tail=j)
+                inp = scan_inputs(rng, pk.tokens, D, dtype, kind == "real")
+                if kind == "positive":
+                    inp["A"][::3, ::5] *= -0.5
+                if kind == "wide":
+                    inp["A"] *= 100.0
+                    inp["delta"][::7] += 12.0
+                    inp["delta"] = synthetic.round_bf16(inp["delta"])
+                state0, y0 = rnd(rng, pk.count, D, N), rnd(rng, pk.tokens, D, dtype=dtype)
+                y_ref, s_ref = scan_reference(pk, inp, state0, y0, gate=j != 1)
+                state, out = dev(state0), dev(y0, dtype)
+                scan_call(pk, inp, state, out, dtype, gate=j != 1)
+                ss.check()
+                for i, rows, slot in pk.each():
+                    # A positive A grows a state by exp(sum delta A): past 3e38
+                    # it leaves fp32, and the exponents' sum X carries a
+                    # relative error of X 2^-23.  Up to 1e4, X < 10 and that
+                    # is about 1e-6; larger states, and the outputs of their
+                    # channels, are not compared.
+                    small = np.abs(s_ref[slot]) <= 1e4
+                    chan = small.all(1)
+                    assert kind == "positive" or small.all()
+                    assert chan.sum() >= D // 2
+                    assert rel(host(state)[slot][small], s_ref[slot][small]) <= 1e-5, (seg, kind, i)
+                    if rows.stop > rows.start:
+                        err = rel(host(out)[rows][:, chan], y_ref[rows][:, chan])
+                        assert err <= (1e-5 if dtype == "f32" else 5e-3), (seg, kind, i)
+    finally:
+        ss.debug_packed_segment(0)
+
+
 def test_scan_packed_many_segments():
     """One long prompt among short ones, few channels: tens of segments per
     sequence, folded between two passes."""
