@@ -776,6 +776,7 @@ struct PackedView {
 struct ConvPackedParams {
     PackedIndex ix;
     int dim, vec, runs, ctiles;
+    int subs;  // kConvRun rows at a time, this many times a run
     int svec;  // the state may be read and written as 16-byte pieces
     const void *x;
     int64_t sx;  // row stride; channels are contiguous
@@ -786,12 +787,14 @@ struct ConvPackedParams {
     int silu;
 };
 
-constexpr int kConvRun = 8;  // rows of a warp
+constexpr int kConvRun = 8;   // rows that a warp holds at once
+constexpr int kConvSubs = 8;  // most of those in a row (64 rows: one mask)
 
-// A warp owns kConvRun rows x 32 CH channels; a block's four warps take
-// neighbouring runs of the same channels.  The rows and the W-1 before them
-// are loaded before the warp knows whose they are; then it walks the sequences
-// in its rows.  A sequence's first W-1 tokens, which
+// A warp owns p.subs times kConvRun rows x 32 CH channels; a block's four
+// warps take neighbouring runs of the same channels.  The first kConvRun rows
+// and the W-1 before them are loaded before the warp knows whose they are;
+// then it walks the sequences in its rows, and each next kConvRun rows are on
+// their way while the last are computed.  A sequence's first W-1 tokens, which
 // need the old state, are all taken by the warp that holds its first row
 // (packed_head), which also writes the new state: no other warp touches the
 // slot.  The other tokens are computed from the loaded rows, under a mask.
@@ -895,7 +898,7 @@ __device__ __forceinline__ void packed_head(const PackedSeq &q, int c0, int dim,
 }
 
 template <typename T, int W, bool VEC>
-__global__ void __launch_bounds__(128, 5) conv_packed_kernel(const __grid_constant__ ConvPackedParams p)
+__global__ void __launch_bounds__(128, 4) conv_packed_kernel(const __grid_constant__ ConvPackedParams p)
 {
     constexpr int CH = VEC ? 16 / int(sizeof(T)) : 4, H = W - 1;
     __shared__ __align__(16) ConvTaps<W, 32 * CH> taps;
@@ -911,7 +914,9 @@ __global__ void __launch_bounds__(128, 5) conv_packed_kernel(const __grid_consta
     T *state = static_cast<T *>(p.state);
     const T zero = conv_zero(static_cast<const T *>(nullptr));
 
-    const int t0 = run * kConvRun, t1 = min(t0 + kConvRun, ix.tokens);
+    const int rows = p.subs * kConvRun;
+    const int t0 = int(min(int64_t(run) * rows, int64_t(ix.tokens)));
+    const int t1 = int(min(int64_t(t0) + rows, int64_t(ix.tokens)));
     const auto fetch = [&](int t, pair_t<T>(&v)[CH / 2]) {
         if (!live || t < 0 || t >= t1) {
 #pragma unroll
@@ -928,7 +933,7 @@ __global__ void __launch_bounds__(128, 5) conv_packed_kernel(const __grid_consta
         }
     };
     pair_t<T> xp[H + kConvRun][CH / 2];
-    if (VEC && live && run < p.runs && t0 >= H && t0 + kConvRun <= ix.tokens) {
+    if (VEC && live && run < p.runs && t0 >= H && t0 + kConvRun <= t1) {
         const T *x = xb + int64_t(t0 - H) * p.sx + c0;
 #pragma unroll
         for (int i = 0; i < H + kConvRun; ++i) {
@@ -974,7 +979,7 @@ __global__ void __launch_bounds__(128, 5) conv_packed_kernel(const __grid_consta
 
     // the sequences in this run: which rows are behind a head, and whether any
     // sequence begins here
-    unsigned mask = 0;
+    uint64_t mask = 0;
     bool heads = false;
     const int s0 = view.find(t0, 1, 0);
     for (int s = s0; s < ix.seqs && view.begin(s) < t1; ++s) {
@@ -982,56 +987,83 @@ __global__ void __launch_bounds__(128, 5) conv_packed_kernel(const __grid_consta
         if (!view.get(s, q) || q.begin >= q.end)
             continue;
         const int lo = max(t0, min(q.end, q.begin + H)) - t0, hi = min(t1, q.end) - t0;
-        if (lo < hi)
-            mask |= (1u << hi) - (1u << lo);
+        if (lo < hi)  // bits lo .. hi - 1
+            mask |= (~uint64_t(0) >> (64 - (hi - lo))) << lo;
         heads |= q.begin >= t0;
     }
-    // pair by pair of channels; the outputs take the places of the inputs
-    with_flag(p.silu, [&](auto silu) {
-#pragma unroll
-        for (int r = 0; r < CH / 2; ++r) {
-            uint64_t w[W], bias, e[W];
-            taps.read(w, bias, lane * CH + 2 * r);
-#pragma unroll
-            for (int k = 0; k < H; ++k)
-                e[k + 1] = PairOf<T>::f2(xp[k][r]);
+    for (int sub = t0; sub < t1 && live; sub += kConvRun) {
+        pair_t<T> nx[kConvRun][CH / 2];
+        if (VEC && sub + 2 * kConvRun <= t1) {
+            const T *x = xb + int64_t(sub + kConvRun) * p.sx + c0;
 #pragma unroll
             for (int i = 0; i < kConvRun; ++i) {
+                load_row<T, CH>(x, nx[i]);
+                x += p.sx;
+            }
+        } else if (sub + kConvRun < t1) {
+#pragma unroll
+            for (int i = 0; i < kConvRun; ++i)
+                fetch(sub + kConvRun + i, nx[i]);
+        }
+        // pair by pair of channels; the outputs take the places of the inputs
+        with_flag(p.silu, [&](auto silu) {
+#pragma unroll
+            for (int r = 0; r < CH / 2; ++r) {
+                uint64_t w[W], bias, e[W];
+                taps.read(w, bias, lane * CH + 2 * r);
 #pragma unroll
                 for (int k = 0; k < H; ++k)
-                    e[k] = e[k + 1];
-                e[H] = PairOf<T>::f2(xp[H + i][r]);
-                uint64_t v = tap_sum<W>(w, e, bias);
-                if (decltype(silu)::value)
-                    v = silu2<T>(v);
-                xp[i][r] = PairOf<T>::round(v);
-            }
-        }
-    });
-    if (VEC && live && mask == (1u << kConvRun) - 1) {
-        T *y = yb + int64_t(t0) * p.sy + c0;
+                    e[k + 1] = PairOf<T>::f2(xp[k][r]);
 #pragma unroll
-        for (int i = 0; i < kConvRun; ++i) {
-            store_row<T, CH>(y, xp[i]);
-            y += p.sy;
-        }
-    } else if (live) {
+                for (int i = 0; i < kConvRun; ++i) {
 #pragma unroll
-        for (int i = 0; i < kConvRun; ++i) {
-            if (!(mask >> i & 1))
-                continue;
-            T *y = yb + int64_t(t0 + i) * p.sy + c0;
-            if (VEC) {
-                store_row<T, CH>(y, xp[i]);
-            } else {
-#pragma unroll
-                for (int r = 0; r < CH / 2; ++r) {
-                    if (c0 + 2 * r < p.dim)
-                        y[2 * r] = PairOf<T>::lo(xp[i][r]);
-                    if (c0 + 2 * r + 1 < p.dim)
-                        y[2 * r + 1] = PairOf<T>::hi(xp[i][r]);
+                    for (int k = 0; k < H; ++k)
+                        e[k] = e[k + 1];
+                    e[H] = PairOf<T>::f2(xp[H + i][r]);
+                    uint64_t v = tap_sum<W>(w, e, bias);
+                    if (decltype(silu)::value)
+                        v = silu2<T>(v);
+                    xp[i][r] = PairOf<T>::round(v);
                 }
             }
+        });
+        const unsigned some = unsigned(mask) & 255u;
+        mask >>= kConvRun;
+        T *y = yb + int64_t(sub) * p.sy + c0;
+        if (VEC && some == 255u) {
+#pragma unroll
+            for (int i = 0; i < kConvRun; ++i) {
+                store_row<T, CH>(y, xp[i]);
+                y += p.sy;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kConvRun; ++i) {
+                if (some >> i & 1) {
+                    if (VEC) {
+                        store_row<T, CH>(y, xp[i]);
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < CH / 2; ++r) {
+                            if (c0 + 2 * r < p.dim)
+                                y[2 * r] = PairOf<T>::lo(xp[i][r]);
+                            if (c0 + 2 * r + 1 < p.dim)
+                                y[2 * r + 1] = PairOf<T>::hi(xp[i][r]);
+                        }
+                    }
+                }
+                y += p.sy;
+            }
+        }
+        // the last W-1 rows go in front of the next
+#pragma unroll
+        for (int r = 0; r < CH / 2; ++r) {
+#pragma unroll
+            for (int i = 0; i < H; ++i)
+                xp[i][r] = xp[kConvRun + i][r];
+#pragma unroll
+            for (int i = 0; i < kConvRun; ++i)
+                xp[H + i][r] = nx[i][r];
         }
     }
     if (!heads)
@@ -1064,8 +1096,7 @@ struct ConvBwdParams {
 // the taps' gradients, and forms dx, for which it needs the first W-1 g of
 // the tokens behind its own: those of the lane that holds the next token
 // block (a shuffle), or, for the warp's last block, of the first block of the
-// tile done before.  Above a run they are recomputed: the run's first step is
-// the block behind it, of which only those W-1 tokens are used.
+// tile done before.  Those behind the run are recomputed first.
 template <typename T, int W, bool XTOK, bool YTOK>
 __global__ void __launch_bounds__(128, 4) conv_bwd_kernel(const __grid_constant__ ConvBwdParams p)
 {
@@ -1099,12 +1130,35 @@ __global__ void __launch_bounds__(128, 4) conv_bwd_kernel(const __grid_constant_
     }
 
     const int64_t first = int64_t(run) * p.steps * tile;
-    for (int step = p.steps; step >= 0; --step) {
+    if (first + int64_t(p.steps) * tile < p.L) {
+        // the first W-1 g behind the run
+        const int t0 = int(first + int64_t(p.steps) * tile);
+        if (tg == 0) {
+            pair_t<T> xp[Q][H + TB], yp[Q][TB];
+            load_block<T, XTOK, CH, TB, H>(xp, p.x, past, H, b, c0, t0, p.dim, p.L);
+            load_block<T, YTOK, CH, TB, 0>(yp, p.dy, nullptr, 0, b, c0, t0, p.dim, p.L);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                uint64_t w[W], bias;
+                taps.read(w, bias, cg * CH + 2 * q);
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    uint64_t e[W];
+#pragma unroll
+                    for (int k = 0; k < W; ++k)
+                        e[k] = PairOf<T>::f2(xp[q][i + k]);
+                    head[q][i] = PairOf<T>::f2(yp[q][i]);
+                    if (p.silu)
+                        head[q][i] = silu_grad2<T>(tap_sum<W>(w, e, bias), head[q][i]);
+                }
+            }
+        }
+    }
+    for (int step = p.steps - 1; step >= 0; --step) {
         const int64_t tl = first + int64_t(step) * tile;  // the tile's first token
         if (tl >= p.L)
             continue;  // nothing there: g is zero (uniform over the warp)
-        const bool above = step == p.steps;  // the block behind the run
-        const int t0 = above && tg ? p.L : int(min(tl + int64_t(tg) * TB, int64_t(p.L)));
+        const int t0 = int(min(tl + int64_t(tg) * TB, int64_t(p.L)));
         pair_t<T> xp[Q][H + TB], yp[Q][TB];
         if (t0 < p.L) {
             load_block<T, XTOK, CH, TB, H>(xp, p.x, past, H, b, c0, t0, p.dim, p.L);
@@ -1140,7 +1194,6 @@ __global__ void __launch_bounds__(128, 4) conv_bwd_kernel(const __grid_constant_
                     g[i] = PairOf<T>::f2(yp[q][i]);
                     if (decltype(silu)::value)
                         g[i] = silu_grad2<T>(tap_sum<W>(w, e, bias), g[i]);
-                    // (the block above a run adds nothing: see below)
 #pragma unroll
                     for (int k = 0; k < W; ++k)
                         dw[q][k] = fma2(g[i], e[k], dw[q][k]);
@@ -1200,16 +1253,7 @@ __global__ void __launch_bounds__(128, 4) conv_bwd_kernel(const __grid_constant_
             for (int i = 0; i < TB; ++i)
                 yp[q][i] = PairOf<T>::round(g[i]);  // dx, in place of dy
         }
-        if (above) {
-#pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                db[q] = 0;
-#pragma unroll
-                for (int k = 0; k < W; ++k)
-                    dw[q][k] = 0;
-            }
-        }
-        if (!above && t0 < p.L)
+        if (t0 < p.L)
             store_block<T, XTOK, CH, TB>(yp, p.dx, b, c0, t0, p.dim, p.L);
     }
     // the run's sums over the warp's token blocks

@@ -139,13 +139,22 @@ void launch_conv_bwd(const ConvBwdParams &p, bool xt, bool yt, dim3 grid, cudaSt
            : conv_bwd_kernel<T, W, false, false><<<grid, 128, 0, s>>>(p);
 }
 
-// Rows of a block of the convolution's single-token kernel: one while the
-// blocks do not fill the GPU several times over, else as many as keep about
-// 1000 blocks (a block's taps are read once for its rows).
-int conv_step_rows(int64_t batch, int64_t gx)
+// Rows of a block of the convolution's single-token kernel: as many as let one
+// wave of blocks (four per SM) hold the batch, at most kConvStepRows.  A
+// block's taps are read once for its rows.
+int conv_step_rows(int64_t batch, int64_t gx, int64_t sms)
 {
-    const int64_t rows = batch * gx / 1024;
-    return rows < 4 ? (batch * gx <= 1024 ? 1 : 4) : rows >= 16 ? 16 : int(rows / 4 * 4);
+    const int64_t rows = (batch * gx + 4 * sms - 1) / (4 * sms);
+    return int(std::min<int64_t>(std::max<int64_t>(rows, 1), kConvStepRows));
+}
+
+// kConvRun rows at a time, how many times a warp of the packed convolution
+// takes them: as few as let one wave of blocks (four per SM) hold the rows.
+int conv_packed_subs(int64_t tokens, int64_t ctiles, int64_t sms)
+{
+    const int64_t blocks = (tokens + 4 * kConvRun - 1) / (4 * kConvRun) * ctiles;
+    return int(std::min<int64_t>(std::max<int64_t>((blocks + 4 * sms - 1) / (4 * sms), 1),
+                                 kConvSubs));
 }
 
 int g_dbg_packed_seg = 0;    // test hooks, see selscan_debug_packed_segment
@@ -156,16 +165,18 @@ struct PackedPlan {
     int seg_len;  // tokens of a segment
 };
 
-// Lanes per channel and tokens per segment of packed prompts.
+// Lanes per channel and tokens per segment of packed prompts (warps: the
+// channels' warps of one sequence).
 PackedPlan packed_plan(int64_t tokens, int64_t seqs, int64_t dim, int64_t sms)
 {
     const int64_t warps1 = (dim + 63) / 64, warps4 = 4 * warps1;
     const auto seg_of = [&](int64_t warps, int64_t slots) {
         return std::max<int64_t>(64, ((tokens * warps + slots - 1) / slots + 15) / 16 * 16);
     };
-    const int64_t seg4 = seg_of(warps4, 24 * sms);
+    const int64_t seg4 = seg_of(warps4, 56 * sms);
     PackedPlan plan;
-    plan.lanes = g_dbg_packed_lanes ? g_dbg_packed_lanes : (tokens > seqs * seg4 ? 1 : 4);
+    plan.lanes = g_dbg_packed_lanes ? g_dbg_packed_lanes
+                                    : (tokens > 4 * seqs * seg4 && seg4 > 64 ? 1 : 4);
     const int64_t seg = plan.lanes == 1 ? seg_of(warps1, 16 * sms) : seg4;
     plan.seg_len = g_dbg_packed_seg ? g_dbg_packed_seg : int(std::min(seg, kMaxLen));
     return plan;
@@ -458,11 +469,12 @@ extern "C" selscan_status selscan_conv_step(selscan_tensor *state, const selscan
         return SELSCAN_OK;
 
     ConvStepParams p{};
+    int dev = 0;
+    DeviceInfo *di = nullptr;
+    if ((st = device_setup(&dev, &di)) != SELSCAN_OK)
+        return st;
+    const int64_t sms = di->sm_count;
     if (slots) {
-        int dev = 0;
-        DeviceInfo *di = nullptr;
-        if ((st = device_setup(&dev, &di)) != SELSCAN_OK)
-            return st;
         p.slots = static_cast<const int *>(slots->data);
         p.err = di->err;
     }
@@ -487,7 +499,7 @@ extern "C" selscan_status selscan_conv_step(selscan_tensor *state, const selscan
     p.silu = silu ? 1 : 0;
     const int64_t threads = p.vec ? dim / blk : dim;
     const int64_t gx = (threads + 127) / 128;
-    p.rows = conv_step_rows(batch, gx);
+    p.rows = conv_step_rows(batch, gx, sms);
     const dim3 grid{unsigned(gx), unsigned((batch + p.rows - 1) / p.rows)};
     dispatch(dt, W, [&](auto tag, auto w) {
         using T = decltype(tag);
@@ -551,9 +563,10 @@ extern "C" selscan_status selscan_conv_packed(selscan_tensor *state, const selsc
     p.bias = static_cast<const float *>(opt_data(bias));
     p.state = state->data;
     p.silu = silu ? 1 : 0;
-    p.runs = int((tokens + kConvRun - 1) / kConvRun);
     const int64_t per = 32 * (p.vec ? blk : 4);
     p.ctiles = int((dim + per - 1) / per);
+    p.subs = conv_packed_subs(tokens, p.ctiles, di->sm_count);
+    p.runs = int((tokens + p.subs * kConvRun - 1) / (p.subs * kConvRun));
     const int64_t blocks = (int64_t(p.runs) + 1 + 3) / 4 * p.ctiles;
     if (blocks > 0x7fffffffll)
         return SELSCAN_ERR_UNSUPPORTED;

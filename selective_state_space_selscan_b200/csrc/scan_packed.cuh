@@ -58,41 +58,19 @@ __device__ __forceinline__ int64_t packed_agg(int begin, int seg_len)
     return 2 * int64_t(begin / seg_len);
 }
 
-// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) <= 1, with log1p(e) = 2
-// atanh(e / (2 + e)): an odd series in s = e / (2 + e) <= 1/3, so that small
-// step sizes keep their relative accuracy (about 5e-7 with the fast e and
-// reciprocal; lg2 of 1 + e would lose 1.5e-5 where e is 2^-6).  The
-// coefficients are a least-maximum fit of 2 atanh(s) / s in s^2 (relative
-// error 4e-9).
-__device__ __forceinline__ uint64_t packed_softplus(uint64_t x)
-{
-    const auto k = [](float v) { return pk2(v, v); };
-    const uint64_t m = mul2(pk2(-fabsf(lo2(x)), -fabsf(hi2(x))), k(kLog2e));
-    const uint64_t e = pk2(ex2_approx(lo2(m)), ex2_approx(hi2(m)));
-    const uint64_t d = add2(e, k(2.f));
-    const uint64_t s = mul2(e, pk2(rcp_approx(lo2(d)), rcp_approx(hi2(d)))), w = mul2(s, s);
-    uint64_t q = k(0.2817833423614502f);
-    q = fma2(q, w, k(0.27960601449012756f));
-    q = fma2(q, w, k(0.40024909377098083f));
-    q = fma2(q, w, k(0.6666631698608398f));
-    q = fma2(q, w, k(2.0f));
-    return fma2(s, q, pk2(fmaxf(lo2(x), 0.f), fmaxf(hi2(x), 0.f)));
-}
-
 // 2^x of a pair in fp32: x = n + f with n the nearest integer, 2^f = 1 + f
 // p(f) (a least-maximum fit on |f| <= 1/2, relative error 3e-9 before rounding,
 // whose first coefficient is ln 2, so that factors next to 1, whose products
 // run over thousands of tokens, are not biased), 2^n added to the exponent.
-// x is held to [-125, 127].
-__device__ __forceinline__ uint64_t exp2_pair(uint64_t x)
+// x is held to [-125, 127]; `rest` is what x lacks.
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t x, uint64_t rest = 0)
 {
     constexpr float kRound = 12582912.f;  // 1.5 * 2^23: integers in the low bits
-    const uint64_t c = pk2(fminf(fmaxf(lo2(x), -125.f), 127.f), fminf(fmaxf(hi2(x), -125.f), 127.f));
-    const uint64_t t = add2(c, pk2(kRound, kRound));
-    const uint64_t f = add2(c, fma2(t, pk2(-1.f, -1.f), pk2(kRound, kRound)));
-    uint64_t q;
     const auto k = [](float v) { return pk2(v, v); };
-    q = k(0.00015324314881581813f);
+    const uint64_t c = pk2(fminf(fmaxf(lo2(x), -125.f), 127.f), fminf(fmaxf(hi2(x), -125.f), 127.f));
+    const uint64_t t = add2(c, k(kRound));
+    const uint64_t f = add2(add2(c, fma2(t, k(-1.f), k(kRound))), rest);
+    uint64_t q = k(0.00015324314881581813f);
     q = fma2(q, f, k(0.0013390958774834871f));
     q = fma2(q, f, k(0.009618517942726612f));
     q = fma2(q, f, k(0.05550359562039375f));
@@ -103,6 +81,69 @@ __device__ __forceinline__ uint64_t exp2_pair(uint64_t x)
         return __uint_as_float(__float_as_uint(v) + (__float_as_uint(n) << 23));
     };
     return pk2(scale(lo2(q), lo2(t)), scale(hi2(q), hi2(t)));
+}
+
+// exp(x) of a pair: the special-function unit for bf16 results; in fp32 x
+// log2 e with what its rounding loses.
+template <typename T>
+__device__ __forceinline__ uint64_t exp_pair(uint64_t x)
+{
+    const uint64_t l = pk2(kLog2e, kLog2e);
+    if constexpr (!std::is_same<T, float>::value) {
+        const uint64_t m = mul2(x, l);
+        return pk2(ex2_approx(lo2(m)), ex2_approx(hi2(m)));
+    } else {
+        // x l - m exactly, and x times the part of log2 e that fp32 does not
+        // hold (x finite: infinities have no such rest)
+        constexpr float kLog2eLo = 1.92596299e-8f;
+        x = pk2(fminf(fmaxf(lo2(x), -87.f), 88.f), fminf(fmaxf(hi2(x), -87.f), 88.f));
+        const uint64_t m = mul2(x, l);
+        const uint64_t lost = fma2(x, l, mul2(m, pk2(-1.f, -1.f)));
+        return exp2_pair(m, fma2(x, pk2(kLog2eLo, kLog2eLo), lost));
+    }
+}
+
+// 1 / d of a pair, d in [1, 2^127]: in fp32 with a Newton step.
+template <typename T>
+__device__ __forceinline__ uint64_t recip_pair(uint64_t d)
+{
+    const uint64_t r = pk2(rcp_approx(lo2(d)), rcp_approx(hi2(d)));
+    if constexpr (!std::is_same<T, float>::value)
+        return r;
+    const uint64_t e = fma2(mul2(d, pk2(-1.f, -1.f)), r, pk2(1.f, 1.f));
+    return fma2(r, e, r);
+}
+
+// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) <= 1, with log1p(e) = 2
+// atanh(e / (2 + e)): an odd series in s = e / (2 + e) <= 1/3, so that small
+// step sizes keep their relative accuracy (about 5e-7 with the fast e and
+// reciprocal; lg2 of 1 + e would lose 1.5e-5 where e is 2^-6).  The
+// coefficients are a least-maximum fit of 2 atanh(s) / s in s^2 (relative
+// error 4e-9).
+template <typename T>
+__device__ __forceinline__ uint64_t softplus_pair(uint64_t x)
+{
+    const auto k = [](float v) { return pk2(v, v); };
+    const uint64_t e = exp_pair<T>(pk2(-fabsf(lo2(x)), -fabsf(hi2(x))));
+    const uint64_t s = mul2(e, recip_pair<T>(add2(e, k(2.f)))), w = mul2(s, s);
+    uint64_t q = k(0.2817833423614502f);
+    q = fma2(q, w, k(0.27960601449012756f));
+    q = fma2(q, w, k(0.40024909377098083f));
+    q = fma2(q, w, k(0.6666631698608398f));
+    q = fma2(q, w, k(2.0f));
+    // NaN passes through the sum; exp_pair in fp32 would hold it to a number
+    const uint64_t r = fma2(s, q, pk2(fmaxf(lo2(x), 0.f), fmaxf(hi2(x), 0.f)));
+    if constexpr (!std::is_same<T, float>::value)
+        return r;
+    return pk2(lo2(x) == lo2(x) ? lo2(r) : lo2(x), hi2(x) == hi2(x) ? hi2(r) : hi2(x));
+}
+
+// z sigmoid(z) of a pair.
+template <typename T>
+__device__ __forceinline__ uint64_t gate_pair(uint64_t z)
+{
+    const uint64_t e = exp_pair<T>(mul2(z, pk2(-1.f, -1.f)));
+    return mul2(z, recip_pair<T>(add2(e, pk2(1.f, 1.f))));
 }
 
 // Shape of a unit.  A thread holds two adjacent channels (one row of B and C
@@ -188,7 +229,6 @@ template <typename T, int LPC, bool SOFT, bool FULL>
 __device__ __forceinline__ SpPrep<4 / LPC> packed_prepare(const SpChannels<LPC> &s, int t0, int n,
                                                           const T *us, const T *ds)
 {
-    constexpr bool kFast = !std::is_same<T, float>::value;
     constexpr int P = SpShape<T, LPC>::kPitch, OWN = 4 / LPC;
     SpPrep<OWN> r;
 #pragma unroll
@@ -196,7 +236,7 @@ __device__ __forceinline__ SpPrep<4 / LPC> packed_prepare(const SpChannels<LPC> 
         const int t = t0 + i * LPC + s.j;
         uint64_t d = add2(packed_two(ds + t * P), s.bias);
         if (SOFT)
-            d = kFast ? packed_softplus(d) : pk2(softplus_exact(lo2(d)), softplus_exact(hi2(d)));
+            d = softplus_pair<T>(d);
         const uint64_t x = mul2(d, packed_two(us + t * P));
         // tokens from n on get a zero step, which leaves the state as it is
         r.dt[i] = FULL || t < n ? d : 0;
@@ -306,8 +346,7 @@ __device__ __forceinline__ void packed_chunk(SpChannels<LPC> &s, int n, const T 
             const int t = t0 + i * LPC + s.j;
             uint64_t v = fma2(s.dskip, packed_two(us + t * P), part[i]);
             if (GATE) {
-                const uint64_t z = packed_two(zs + t * P);
-                v = mul2(v, silu2<T>(z));
+                v = mul2(v, gate_pair<T>(packed_two(zs + t * P)));
             }
             if (FULL || t < n)
                 packed_store(y + t * sy, v, s.chans, s.pair);
