@@ -173,10 +173,12 @@ PackedPlan packed_plan(int64_t tokens, int64_t seqs, int64_t dim, int64_t sms)
     const auto seg_of = [&](int64_t warps, int64_t slots) {
         return std::max<int64_t>(64, ((tokens * warps + slots - 1) / slots + 15) / 16 * 16);
     };
-    const int64_t seg4 = seg_of(warps4, 56 * sms);
+    // a few short sequences: one segment each, one launch
+    const int64_t seg4 =
+        tokens <= 512 && tokens <= 64 * seqs ? tokens + 1 : seg_of(warps4, 28 * sms);
     PackedPlan plan;
     plan.lanes = g_dbg_packed_lanes ? g_dbg_packed_lanes
-                                    : (tokens > 4 * seqs * seg4 && seg4 > 64 ? 1 : 4);
+                                    : (tokens > 2 * seqs * seg4 && seg4 > 64 ? 1 : 4);
     const int64_t seg = plan.lanes == 1 ? seg_of(warps1, 16 * sms) : seg4;
     plan.seg_len = g_dbg_packed_seg ? g_dbg_packed_seg : int(std::min(seg, kMaxLen));
     return plan;

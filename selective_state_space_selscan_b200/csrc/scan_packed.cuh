@@ -159,11 +159,11 @@ template <typename T, int LPC>
 struct SpShape {
     static constexpr int kCT = 64;  // channels
     static constexpr int kThreads = kCT / 2 * LPC;
-    static constexpr int kTC = 32 / int(sizeof(T));  // tokens staged at once
+    static constexpr int kTC = (LPC == 4 ? 64 : 32) / int(sizeof(T));  // tokens staged at once
     // row pitch: with LPC lanes per channel a warp reads LPC rows at once;
     // 128 / LPC bytes more put them into different banks
     static constexpr int kPitch = kCT + (LPC == 1 ? 0 : 128 / LPC / int(sizeof(T)));
-    static constexpr int kBlocks = LPC == 1 ? 12 : LPC == 2 ? 8 : 6;  // resident per SM
+    static constexpr int kBlocks = LPC == 1 ? 12 : LPC == 2 ? 8 : 4;  // resident per SM
 };
 
 // What a thread holds of its two channels.
