@@ -519,18 +519,24 @@ struct ConvStepParams {
 
 // One token of every row: e = [state | x], the state shifted by one.  A
 // thread owns CH channels, whose (W-1) CH state elements are W-1 whole 16-byte
-// vectors (VEC), or one channel (any strides, any dim), of RB rows at a time:
-// its taps serve all of a block's rows, and the loads of RB rows are in flight
-// at once.  Slots as in the scan's decode step: negative is padding, a slot
-// past the end or owned by an earlier row is refused.
+// vectors (VEC), or one channel (any strides, any dim); its taps serve all of
+// a block's rows.  A warp's state of a row is one contiguous piece: it comes
+// and goes through shared memory in whole lines (the threads' own vectors lie
+// W-1 vectors apart, and stores of 16 bytes out of every 48 cost the L2 twice
+// the sectors: 23.6 us, now 18.0, for 1024 rows of 5120), kStepDepth rows on
+// their way at a time.  Slots as in the scan's decode step: negative is
+// padding, a slot past the end or owned by an earlier row is refused.
 constexpr int kConvStepRows = 16;  // most rows of a block
+constexpr int kStepDepth = 4;
 
-template <typename T, int W, bool VEC, int RB>
+template <typename T, int W, bool VEC>
 __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ ConvStepParams p)
 {
     constexpr int CH = VEC ? 16 / int(sizeof(T)) : 1, NV = W - 1;
     __shared__ int row_s[kConvStepRows];  // the row's place in the cache, or -1
-    const int tid = threadIdx.x;
+    // [warp][row][the state's vectors, then x's]
+    __shared__ uint4 ring[4][VEC ? kStepDepth : 1][VEC ? 32 * (NV + 1) : 1];
+    const int tid = threadIdx.x, lane = tid & 31;
     const int c0 = (int(blockIdx.x) * 128 + tid) * CH;
     const bool live = c0 < p.dim;
     const int b0 = int(blockIdx.y) * p.rows, nb = min(p.rows, p.batch - b0);
@@ -568,71 +574,29 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ 
 
     const T *x = static_cast<const T *>(p.x) + c0 * p.sx1;
     T *y = static_cast<T *>(p.y) + c0 * p.sy1;
-    T *state = static_cast<T *>(p.state) + int64_t(c0) * NV;
-    struct Rows {
-        alignas(16) T raw[RB][NV * CH];
-        alignas(16) T x[RB][CH];
-    };
-    const auto load = [&](Rows &r, int i0) {
+    // the warp's piece of a state row, and how many vectors of it there are
+    const int cw = (int(blockIdx.x) * 128 + (tid & ~31)) * CH;
+    const int vecs = VEC ? max(0, min(32, (p.dim - cw) / CH)) * NV : 0;
+    T *state = static_cast<T *>(p.state) + int64_t(VEC ? cw : c0) * NV;
+    uint4(*mine)[VEC ? 32 * (NV + 1) : 1] = ring[tid >> 5];
+    const auto fetch = [&](int i) {
+        const int row = i < nb ? row_s[i] : -1;
+        if (VEC && row >= 0) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(state + int64_t(row) * p.dim * NV);
+            uint4 *dst = mine[i % kStepDepth];
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-            const int row = i0 + i < nb ? row_s[i0 + i] : -1;
-            if (row < 0 || !live)
-                continue;
-            const T *st = state + int64_t(row) * p.dim * NV;
-            const T *xi = x + (b0 + i0 + i) * p.sx0;
-            if constexpr (VEC) {
-#pragma unroll
-                for (int k = 0; k < NV; ++k)
-                    *reinterpret_cast<uint4 *>(r.raw[i] + k * CH) =
-                        reinterpret_cast<const uint4 *>(st)[k];
-                *reinterpret_cast<uint4 *>(r.x[i]) = *reinterpret_cast<const uint4 *>(xi);
-            } else {
-#pragma unroll
-                for (int k = 0; k < NV; ++k)
-                    r.raw[i][k] = st[k];
-                r.x[i][0] = xi[0];
-            }
+            for (int k = 0; k < NV; ++k)
+                if (k * 32 + lane < vecs)
+                    cp_async16(dst + k * 32 + lane, src + k * 32 + lane, 16);
+            if (live)
+                cp_async16(dst + NV * 32 + lane, x + (b0 + i) * p.sx0, 16);
         }
+        cp_async_commit();
     };
-    const auto step = [&](const Rows &r, int i0) {
+    if (VEC)
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-            const int row = i0 + i < nb ? row_s[i0 + i] : -1;
-            if (row < 0)
-                continue;
-            alignas(16) T yr[CH], sr[NV * CH];
-#pragma unroll
-            for (int j = 0; j < CH; ++j) {
-                float v = bias[j];
-#pragma unroll
-                for (int k = 0; k < NV; ++k)
-                    v = fmaf(w[j * W + k], float(r.raw[i][j * NV + k]), v);
-                v = fmaf(w[j * W + NV], float(r.x[i][j]), v);
-                if (p.silu)
-                    v = std::is_same<T, float>::value ? silu_exact(v) : silu_fast(v);
-                yr[j] = T(v);
-#pragma unroll
-                for (int k = 0; k < NV; ++k)
-                    sr[j * NV + k] = k + 1 < NV ? r.raw[i][j * NV + (k + 1 < NV ? k + 1 : 0)] : r.x[i][j];
-            }
-            T *st = state + int64_t(row) * p.dim * NV;
-            T *yi = y + (b0 + i0 + i) * p.sy0;
-            if constexpr (VEC) {
-#pragma unroll
-                for (int k = 0; k < NV; ++k)
-                    reinterpret_cast<uint4 *>(st)[k] = *reinterpret_cast<uint4 *>(sr + k * CH);
-                *reinterpret_cast<uint4 *>(yi) = *reinterpret_cast<uint4 *>(yr);
-            } else {
-#pragma unroll
-                for (int k = 0; k < NV; ++k)
-                    st[k] = sr[k];
-                yi[0] = yr[0];
-            }
-        }
-    };
-    Rows ra, rb;
-    load(ra, 0);
+        for (int i = 0; i < kStepDepth - 1; ++i)
+            fetch(i);
 
     if (p.slots) {
         // earlier rows with one of this block's slots, eight loads at a time
@@ -643,10 +607,10 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ 
             for (int m = 0; m < 8; ++m)
                 other[m] = j0 + m * 128 < b0 + nb - 1 ? p.slots[j0 + m * 128] : -1;
             for (int i = 0; i < nb; ++i) {
-                const int mine = row_s[i];
+                const int own = row_s[i];
 #pragma unroll
                 for (int m = 0; m < 8; ++m)
-                    if (other[m] >= 0 && other[m] == mine && j0 + m * 128 < b0 + i)
+                    if (other[m] >= 0 && other[m] == own && j0 + m * 128 < b0 + i)
                         bad |= 1u << i;
             }
         }
@@ -658,16 +622,72 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ 
             }
         __syncthreads();
     }
-    if (!live)
-        return;
-    // the next rows are on their way while these are worked on
-    for (int i0 = 0; i0 < nb; i0 += 2 * RB) {
-        if (p.rows > RB)
-            load(rb, i0 + RB);
-        step(ra, i0);
-        if (p.rows > RB) {
-            load(ra, i0 + 2 * RB);
-            step(rb, i0 + RB);
+    // one channel: state and input in, output and state out
+    const auto channel = [&](const T(&e)[W], int j, T(&next)[NV]) -> T {
+        float v = bias[j];
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            v = fmaf(w[j * W + k], float(e[k]), v);
+        if (p.silu)
+            v = std::is_same<T, float>::value ? silu_exact(v) : silu_fast(v);
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            next[k] = e[k + 1];
+        return T(v);
+    };
+    if constexpr (!VEC) {
+        for (int i = 0; i < nb && live; ++i) {
+            if (row_s[i] < 0)
+                continue;
+            T *st = state + int64_t(row_s[i]) * p.dim * NV;
+            T e[W], next[NV];
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                e[k] = st[k];
+            e[NV] = x[(b0 + i) * p.sx0];
+            y[(b0 + i) * p.sy0] = channel(e, 0, next);
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                st[k] = next[k];
+        }
+    } else {
+        for (int i = 0; i < nb; ++i) {
+            fetch(i + kStepDepth - 1);
+            cp_async_wait<kStepDepth - 1>();
+            __syncwarp();
+            const int row = row_s[i];
+            if (row < 0)
+                continue;  // the same for the whole block
+            uint4 *buf = mine[i % kStepDepth];
+            alignas(16) T raw[NV * CH], xr[CH], yr[CH];
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                *reinterpret_cast<uint4 *>(raw + k * CH) = buf[lane * NV + k];
+            *reinterpret_cast<uint4 *>(xr) = buf[NV * 32 + lane];
+#pragma unroll
+            for (int j = 0; j < CH; ++j) {
+                T e[W], next[NV];
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    e[k] = raw[j * NV + k];
+                e[NV] = xr[j];
+                yr[j] = channel(e, j, next);
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    raw[j * NV + k] = next[k];
+            }
+            if (live)
+                *reinterpret_cast<uint4 *>(y + (b0 + i) * p.sy0) = *reinterpret_cast<uint4 *>(yr);
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                buf[lane * NV + k] = *reinterpret_cast<uint4 *>(raw + k * CH);
+            __syncwarp();
+            uint4 *dst = reinterpret_cast<uint4 *>(state + int64_t(row) * p.dim * NV);
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                if (k * 32 + lane < vecs)
+                    dst[k * 32 + lane] = buf[k * 32 + lane];
+            __syncwarp();  // before the next row comes into this place
         }
     }
 }

@@ -506,12 +506,8 @@ extern "C" selscan_status selscan_conv_step(selscan_tensor *state, const selscan
     dispatch(dt, W, [&](auto tag, auto w) {
         using T = decltype(tag);
         constexpr int WW = decltype(w)::value;
-        if (p.vec)
-            p.rows == 1 ? conv_step_kernel<T, WW, true, 1><<<grid, 128, 0, stream>>>(p)
-                        : conv_step_kernel<T, WW, true, 2><<<grid, 128, 0, stream>>>(p);
-        else
-            p.rows == 1 ? conv_step_kernel<T, WW, false, 1><<<grid, 128, 0, stream>>>(p)
-                        : conv_step_kernel<T, WW, false, 2><<<grid, 128, 0, stream>>>(p);
+        p.vec ? conv_step_kernel<T, WW, true><<<grid, 128, 0, stream>>>(p)
+              : conv_step_kernel<T, WW, false><<<grid, 128, 0, stream>>>(p);
     });
     return counted_launch() == cudaSuccess ? SELSCAN_OK : SELSCAN_ERR_CUDA;
 }
