@@ -127,6 +127,83 @@ struct ConvView {
     int vec;
 };
 
+// A block of tokens [t0 - HLO, t0 + TB) x CH channels as its vectors in
+// memory: rows of CH channels (TOK), or, per channel, 16-byte pieces of time
+// (with HLO, the piece before the block too).
+template <typename T, bool TOK, int CH, int TB, int HLO>
+struct BlockIO {
+    static constexpr int VEC = 16 / int(sizeof(T));
+    static constexpr int PER = TB / VEC + (HLO > 0);  // pieces of a channel
+    static constexpr int N = TOK ? HLO + TB : CH * PER;
+    static constexpr int BYTES = TOK ? CH * int(sizeof(T)) : 16;
+    using Piece = std::conditional_t<BYTES == 16, uint4, uint2>;
+    static_assert(BYTES == 16 || BYTES == 8, "pieces of 8 or 16 bytes");
+    static_assert(TOK || TB % VEC == 0, "whole 16-byte pieces of a time row");
+
+    // Whether all of it is inside the tensor, in whole aligned vectors.
+    static __device__ __forceinline__ bool inside(const ConvView &v, int c0, int t0, int dim, int L)
+    {
+        return v.vec && c0 + CH <= dim && t0 >= (HLO ? (TOK ? HLO : VEC) : 0) && t0 + TB <= L;
+    }
+    // f(piece's number, its address)
+    template <typename F>
+    static __device__ __forceinline__ void each(const ConvView &v, int b, int c0, int t0, F f)
+    {
+        const T *base = static_cast<const T *>(v.data) + b * v.sb;
+        if (TOK) {
+            const T *r = base + c0 + (t0 - HLO) * v.st;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                f(i, r);
+                r += v.st;
+            }
+        } else {
+            const T *r = base + c0 * v.sd + t0 - (HLO ? VEC : 0);
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    f(c * PER + j, r + j * VEC);
+                r += v.sd;
+            }
+        }
+    }
+    static __device__ __forceinline__ void unpack(const Piece (&w)[N],
+                                                  pair_t<T> (&xp)[CH / 2][HLO + TB])
+    {
+        if constexpr (TOK) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                pair_t<T> r[CH / 2];
+                load_row<T, CH>(reinterpret_cast<const T *>(&w[i]), r);
+#pragma unroll
+                for (int q = 0; q < CH / 2; ++q)
+                    xp[q][i] = r[q];
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < CH / 2; ++q)
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    const uint4 x = w[2 * q * PER + j], y = w[(2 * q + 1) * PER + j];
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+                    // the piece's first token, counted from the block's halo
+                    const int i0 = HLO ? HLO + (j - 1) * VEC : j * VEC;
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i)
+                        if (i0 + i >= 0) {
+                            pair_t<T> o;
+                            if constexpr (sizeof(T) == 2)
+                                o = __byte_perm(xs[i / 2], ys[i / 2], i % 2 ? 0x7632 : 0x5410);
+                            else
+                                o = uint64_t(xs[i]) | (uint64_t(ys[i]) << 32);
+                            xp[q][i0 + i < 0 ? 0 : i0 + i] = o;
+                        }
+                }
+        }
+    }
+};
+
 // Tokens [t0 - HLO, t0 + TB) of CH channels from c0 of batch row b, as pairs
 // xp[channel pair][token].  Tokens before 0 come from `past` (row (b, c) of
 // W-1 elements, HLO <= W-1) or are zero, tokens from L on and channels from
@@ -136,10 +213,17 @@ __device__ __forceinline__ void load_block(pair_t<T> (&xp)[CH / 2][HLO + TB], co
                                            const T *past, int past_n, int b, int c0, int t0,
                                            int dim, int L)
 {
-    constexpr int VEC = 16 / int(sizeof(T));
+    using IO = BlockIO<T, TOK, CH, TB, HLO>;
+    if (IO::inside(v, c0, t0, dim, L)) {
+        typename IO::Piece w[IO::N];
+        IO::each(v, b, c0, t0, [&](int i, const T *r) {
+            w[i] = *reinterpret_cast<const typename IO::Piece *>(r);
+        });
+        IO::unpack(w, xp);
+        return;
+    }
     const T *base = static_cast<const T *>(v.data) + b * v.sb;
     const T zero = conv_zero(static_cast<const T *>(nullptr));
-    const bool whole_c = c0 + CH <= dim;
     const auto at = [&](int c, int t) -> T {
         if (c >= dim || t >= L)
             return zero;
@@ -147,78 +231,6 @@ __device__ __forceinline__ void load_block(pair_t<T> (&xp)[CH / 2][HLO + TB], co
             return past ? past[(int64_t(b) * dim + c) * past_n + past_n + t] : zero;
         return base[c * v.sd + t * v.st];
     };
-    if (TOK) {
-        if (v.vec && whole_c && t0 >= HLO && t0 + TB <= L) {
-            const T *r = base + c0 + (t0 - HLO) * v.st;
-#pragma unroll
-            for (int i = 0; i < HLO + TB; ++i) {
-                pair_t<T> w[CH / 2];
-                load_row<T, CH>(r, w);
-                r += v.st;
-#pragma unroll
-                for (int q = 0; q < CH / 2; ++q)
-                    xp[q][i] = w[q];
-            }
-            return;
-        }
-        if (v.vec && whole_c && (t0 >= HLO || !past)) {
-#pragma unroll
-            for (int i = 0; i < HLO + TB; ++i) {
-                const int t = t0 - HLO + i;
-                pair_t<T> w[CH / 2];
-#pragma unroll
-                for (int q = 0; q < CH / 2; ++q)
-                    w[q] = 0;
-                if (t >= 0 && t < L)
-                    load_row<T, CH>(base + c0 + t * v.st, w);
-#pragma unroll
-                for (int q = 0; q < CH / 2; ++q)
-                    xp[q][i] = w[q];
-            }
-            return;
-        }
-    } else if (v.vec && whole_c && t0 + TB <= L && (t0 >= VEC || !past || HLO == 0)) {
-        static_assert(TB % VEC == 0, "whole 16-byte pieces of a time row");
-#pragma unroll
-        for (int q = 0; q < CH / 2; ++q) {
-            const T *r0 = base + (c0 + 2 * q) * v.sd + t0;
-            const T *r1 = r0 + v.sd;
-            const auto put = [&](const T *a, const T *bb, int i0, int from) {
-                // VEC tokens of two channels; the first `from` of them are dropped
-                if constexpr (sizeof(T) == 2) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(a);
-                    const uint4 y = *reinterpret_cast<const uint4 *>(bb);
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        if (i >= from)
-                            xp[q][i0 + i - from] =
-                                __byte_perm(xs[i / 2], ys[i / 2], i % 2 ? 0x7632 : 0x5410);
-                } else {
-                    const float4 x = *reinterpret_cast<const float4 *>(a);
-                    const float4 y = *reinterpret_cast<const float4 *>(bb);
-                    const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        if (i >= from)
-                            xp[q][i0 + i - from] = pk2(xs[i], ys[i]);
-                }
-            };
-            if (HLO > 0) {
-                if (t0 >= VEC) {
-                    put(r0 - VEC, r1 - VEC, 0, VEC - HLO);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < HLO; ++i)
-                        xp[q][i] = 0;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < TB / VEC; ++j)
-                put(r0 + j * VEC, r1 + j * VEC, HLO + j * VEC, 0);
-        }
-        return;
-    }
 #pragma unroll
     for (int q = 0; q < CH / 2; ++q)
 #pragma unroll
@@ -1116,12 +1128,22 @@ struct ConvBwdParams {
 // the taps' gradients, and forms dx, for which it needs the first W-1 g of
 // the tokens behind its own: those of the lane that holds the next token
 // block (a shuffle), or, for the warp's last block, of the first block of the
-// tile done before.  Those behind the run are recomputed first.
+// tile done before.  Those behind the run are recomputed first.  The next
+// tile's vectors are on their way into shared memory, each lane's into places
+// of its own, while a tile is computed.
+constexpr int conv_bwd_ch(bool xtok, bool ytok) { return xtok || ytok ? 4 : 2; }
+
 template <typename T, int W, bool XTOK, bool YTOK>
 __global__ void __launch_bounds__(128, 4) conv_bwd_kernel(const __grid_constant__ ConvBwdParams p)
 {
-    constexpr int CH = 4, TB = 16 / int(sizeof(T)), Q = CH / 2, H = W - 1;
+    constexpr int CH = conv_bwd_ch(XTOK, YTOK), TB = 16 / int(sizeof(T)), Q = CH / 2, H = W - 1;
+    using XIO = BlockIO<T, XTOK, CH, TB, H>;
+    using YIO = BlockIO<T, YTOK, CH, TB, 0>;
+    // what fits into 48 KB beside the taps
+    constexpr bool RING = (XIO::N * XIO::BYTES + YIO::N * YIO::BYTES) * 32 * 8 <= 46000;
     __shared__ __align__(16) ConvTaps<W, 32 * CH> taps;
+    __shared__ typename XIO::Piece xring[RING ? 4 : 1][RING ? 2 : 1][RING ? XIO::N : 1][RING ? 32 : 1];
+    __shared__ typename YIO::Piece yring[RING ? 4 : 1][RING ? 2 : 1][RING ? YIO::N : 1][RING ? 32 : 1];
     const int lane = threadIdx.x & 31;
     const int ngr = 32 >> p.cg_log2;  // token blocks of a tile
     const int cg = lane & ((1 << p.cg_log2) - 1), tg = lane >> p.cg_log2;
@@ -1174,13 +1196,50 @@ __global__ void __launch_bounds__(128, 4) conv_bwd_kernel(const __grid_constant_
             }
         }
     }
+    // this lane's first token of a tile
+    const auto start = [&](int step) {
+        return int(min(first + int64_t(step) * tile + int64_t(tg) * TB, int64_t(p.L)));
+    };
+    const auto staged = [&](int t0) {
+        return RING && XIO::inside(p.x, c0, t0, p.dim, p.L) && YIO::inside(p.dy, c0, t0, p.dim, p.L);
+    };
+    const int wp = RING ? int(threadIdx.x >> 5) : 0, ln = RING ? lane : 0;
+    const auto fetch = [&](int step) {
+        if constexpr (RING) {
+            const int t0 = step >= 0 ? start(step) : p.L;
+            if (staged(t0)) {
+                XIO::each(p.x, b, c0, t0, [&](int i, const T *r) {
+                    cp_async_ca<XIO::BYTES>(&xring[wp][step & 1][i][ln], r);
+                });
+                YIO::each(p.dy, b, c0, t0, [&](int i, const T *r) {
+                    cp_async_ca<YIO::BYTES>(&yring[wp][step & 1][i][ln], r);
+                });
+            }
+            cp_async_commit();
+        }
+    };
+    fetch(p.steps - 1);
     for (int step = p.steps - 1; step >= 0; --step) {
+        fetch(step - 1);
         const int64_t tl = first + int64_t(step) * tile;  // the tile's first token
+        if (RING)
+            cp_async_wait<1>();
         if (tl >= p.L)
             continue;  // nothing there: g is zero (uniform over the warp)
-        const int t0 = int(min(tl + int64_t(tg) * TB, int64_t(p.L)));
+        const int t0 = start(step);
         pair_t<T> xp[Q][H + TB], yp[Q][TB];
-        if (t0 < p.L) {
+        if (RING && staged(t0)) {
+            typename XIO::Piece xw[XIO::N];
+            typename YIO::Piece yw[YIO::N];
+#pragma unroll
+            for (int i = 0; i < XIO::N; ++i)
+                xw[i] = xring[wp][step & (RING ? 1 : 0)][RING ? i : 0][ln];
+#pragma unroll
+            for (int i = 0; i < YIO::N; ++i)
+                yw[i] = yring[wp][step & (RING ? 1 : 0)][RING ? i : 0][ln];
+            XIO::unpack(xw, xp);
+            YIO::unpack(yw, yp);
+        } else if (t0 < p.L) {
             load_block<T, XTOK, CH, TB, H>(xp, p.x, past, H, b, c0, t0, p.dim, p.L);
             load_block<T, YTOK, CH, TB, 0>(yp, p.dy, nullptr, 0, b, c0, t0, p.dim, p.L);
         } else {

@@ -390,7 +390,7 @@ extern "C" selscan_status selscan_conv_bwd(const selscan_tensor *x, const selsca
     if ((st = device_setup(&dev, &di)) != SELSCAN_OK)
         return st;
     const bool xt = token_major(x), yt = token_major(dy);
-    const int64_t ch = 4, blk = 16 / int64_t(elem_size(dt));
+    const int64_t ch = conv_bwd_ch(xt, yt), blk = 16 / int64_t(elem_size(dt));
     const int64_t cblocks = (dim + ch - 1) / ch, tblocks = (L + blk - 1) / blk;
     ConvBwdParams p{};
     p.batch = int(batch);

@@ -220,6 +220,14 @@ __device__ __forceinline__ void cp_async16(void *smem_dst, const void *gsrc, uin
                  :: "r"(smem_addr(smem_dst)), "l"(gsrc), "r"(src_bytes) : "memory");
 }
 
+// 8 or 16 bytes by way of the L1 (neighbouring threads read them again).
+template <int BYTES>
+__device__ __forceinline__ void cp_async_ca(void *smem_dst, const void *gsrc)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;"
+                 :: "r"(smem_addr(smem_dst)), "l"(gsrc), "n"(BYTES) : "memory");
+}
+
 __device__ __forceinline__ void cp_async_commit()
 {
     asm volatile("cp.async.commit_group;" ::: "memory");

@@ -145,26 +145,36 @@ __global__ void __launch_bounds__(256, SCALAR ? 8 : 6) step_kernel(StepParams p)
         const int slot = p.slots[b];
         if (slot < 0)
             return;
-        bool bad = slot >= p.slot_count;
-        for (int j = int(threadIdx.x); j < b; j += 256)
-            bad |= p.slots[j] == slot;
-        if (__syncthreads_or(bad)) {
+        if (slot >= p.slot_count) {
             if (threadIdx.x == 0)
                 atomicOr(p.err, kErrIndex);
             return;
         }
         row = slot;
     }
+    // the state comes first: the earlier rows' slots are looked at meanwhile
+    const int64_t ch = row * p.dim + c;
+    float4 *sp = reinterpret_cast<float4 *>(p.state + ch * N);
+    float4 h[V];
+    if (live) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            h[v] = __ldcs(sp + k + v * TPC);
+    }
+    if (SLOTS) {
+        bool bad = false;
+        for (int j = int(threadIdx.x); j < b; j += 256)
+            bad |= p.slots[j] == int(row);
+        if (__syncthreads_or(bad)) {
+            if (threadIdx.x == 0)
+                atomicOr(p.err, kErrIndex);
+            return;
+        }
+    }
 
     float acc = 0.f, x = 0.f;
     if (live) {
         const int g = p.per_group == p.units ? 0 : unit / p.per_group;
-        const int64_t ch = row * p.dim + c;
-        float4 *sp = reinterpret_cast<float4 *>(p.state + ch * N);
-        float4 h[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            h[v] = __ldcs(sp + k + v * TPC);
         float dt = SCALAR ? static_cast<const float *>(p.delta)[b * p.sd0 + unit * p.sd1]
                           : step_load(p.delta, b * p.sd0 + unit * p.sd1, tag);
         x = step_load(p.u, b * p.su0 + c * p.su1, tag);
