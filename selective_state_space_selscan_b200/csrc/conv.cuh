@@ -168,37 +168,57 @@ struct BlockIO {
             }
         }
     }
-    static __device__ __forceinline__ void unpack(const Piece (&w)[N],
-                                                  pair_t<T> (&xp)[CH / 2][HLO + TB])
+    // One pair of channels of a time layout from its two channels' pieces, the
+    // first at w[0], each `step` after the one before.
+    static __device__ __forceinline__ void pair(const Piece *w, int step, pair_t<T> (&o)[HLO + TB])
+    {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const uint4 x = w[j * step], y = w[(PER + j) * step];
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+            // the piece's first token, counted from the block's halo
+            const int i0 = HLO ? HLO + (j - 1) * VEC : j * VEC;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (i0 + i >= 0) {
+                    if constexpr (sizeof(T) == 2)
+                        o[i0 + i < 0 ? 0 : i0 + i] =
+                            __byte_perm(xs[i / 2], ys[i / 2], i % 2 ? 0x7632 : 0x5410);
+                    else
+                        o[i0 + i < 0 ? 0 : i0 + i] = uint64_t(xs[i]) | (uint64_t(ys[i]) << 32);
+                }
+        }
+    }
+    // A lane's pieces in shared memory, 32 places apart: pair q of its channels
+    static __device__ __forceinline__ void take(const Piece *w, int q, pair_t<T> (&o)[HLO + TB])
     {
         if constexpr (TOK) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                pair_t<T> r[CH / 2];
-                load_row<T, CH>(reinterpret_cast<const T *>(&w[i]), r);
+            for (int i = 0; i < N; ++i)
+                o[i] = reinterpret_cast<const pair_t<T> *>(w + i * 32)[q];
+        } else {
+            pair(w + 2 * q * PER * 32, 32, o);
+        }
+    }
+    // and pairs into such pieces (what lies before the halo is left out)
+    static __device__ __forceinline__ void give(Piece *w, const pair_t<T> (&xp)[CH / 2][HLO + TB])
+    {
+        if constexpr (TOK) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
 #pragma unroll
                 for (int q = 0; q < CH / 2; ++q)
-                    xp[q][i] = r[q];
-            }
+                    reinterpret_cast<pair_t<T> *>(w + i * 32)[q] = xp[q][i];
         } else {
 #pragma unroll
             for (int q = 0; q < CH / 2; ++q)
 #pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    const uint4 x = w[2 * q * PER + j], y = w[(2 * q + 1) * PER + j];
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-                    // the piece's first token, counted from the block's halo
-                    const int i0 = HLO ? HLO + (j - 1) * VEC : j * VEC;
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i)
-                        if (i0 + i >= 0) {
-                            pair_t<T> o;
-                            if constexpr (sizeof(T) == 2)
-                                o = __byte_perm(xs[i / 2], ys[i / 2], i % 2 ? 0x7632 : 0x5410);
-                            else
-                                o = uint64_t(xs[i]) | (uint64_t(ys[i]) << 32);
-                            xp[q][i0 + i < 0 ? 0 : i0 + i] = o;
-                        }
+                for (int i = 0; i < HLO + TB; ++i) {
+                    const int at = (HLO ? VEC - HLO : 0) + i;  // in the channel's pieces
+                    T *lo = reinterpret_cast<T *>(w + (2 * q * PER + at / VEC) * 32) + at % VEC;
+                    T *hi = reinterpret_cast<T *>(w + ((2 * q + 1) * PER + at / VEC) * 32) + at % VEC;
+                    *lo = PairOf<T>::lo(xp[q][i]);
+                    *hi = PairOf<T>::hi(xp[q][i]);
                 }
         }
     }
@@ -215,11 +235,23 @@ __device__ __forceinline__ void load_block(pair_t<T> (&xp)[CH / 2][HLO + TB], co
 {
     using IO = BlockIO<T, TOK, CH, TB, HLO>;
     if (IO::inside(v, c0, t0, dim, L)) {
-        typename IO::Piece w[IO::N];
-        IO::each(v, b, c0, t0, [&](int i, const T *r) {
-            w[i] = *reinterpret_cast<const typename IO::Piece *>(r);
-        });
-        IO::unpack(w, xp);
+        if constexpr (TOK) {
+            IO::each(v, b, c0, t0, [&](int i, const T *r) {
+                pair_t<T> w[CH / 2];
+                load_row<T, CH>(r, w);
+#pragma unroll
+                for (int q = 0; q < CH / 2; ++q)
+                    xp[q][i] = w[q];
+            });
+        } else {
+            typename IO::Piece w[IO::N];
+            IO::each(v, b, c0, t0, [&](int i, const T *r) {
+                w[i] = *reinterpret_cast<const typename IO::Piece *>(r);
+            });
+#pragma unroll
+            for (int q = 0; q < CH / 2; ++q)
+                IO::pair(w + 2 * q * IO::PER, 1, xp[q]);
+        }
         return;
     }
     const T *base = static_cast<const T *>(v.data) + b * v.sb;
@@ -231,6 +263,44 @@ __device__ __forceinline__ void load_block(pair_t<T> (&xp)[CH / 2][HLO + TB], co
             return past ? past[(int64_t(b) * dim + c) * past_n + past_n + t] : zero;
         return base[c * v.sd + t * v.st];
     };
+    if (v.vec && c0 + CH <= dim && (TOK || t0 + TB <= L)) {
+        // an end of the sequence: whole vectors inside, the rest as it comes
+#pragma unroll
+        for (int q = 0; q < CH / 2; ++q)
+#pragma unroll
+            for (int i = 0; i < HLO + (TOK ? TB : 0); ++i)
+                xp[q][i] = t0 - HLO + i < 0 && past
+                               ? PairOf<T>::make(at(c0 + 2 * q, t0 - HLO + i),
+                                                 at(c0 + 2 * q + 1, t0 - HLO + i))
+                               : pair_t<T>(0);
+        if constexpr (TOK) {
+#pragma unroll
+            for (int i = 0; i < HLO + TB; ++i)
+                if (t0 - HLO + i >= 0 && t0 - HLO + i < L) {
+                    pair_t<T> w[CH / 2];
+                    load_row<T, CH>(base + c0 + (t0 - HLO + i) * v.st, w);
+#pragma unroll
+                    for (int q = 0; q < CH / 2; ++q)
+                        xp[q][i] = w[q];
+                }
+        } else {
+            // (the block at token 0: nothing before it is in the tensor)
+            using Inner = BlockIO<T, TOK, CH, TB, 0>;
+            typename Inner::Piece w[Inner::N];
+            Inner::each(v, b, c0, t0, [&](int i, const T *r) {
+                w[i] = *reinterpret_cast<const typename Inner::Piece *>(r);
+            });
+#pragma unroll
+            for (int q = 0; q < CH / 2; ++q) {
+                pair_t<T> o[TB];
+                Inner::pair(w + 2 * q * Inner::PER, 1, o);
+#pragma unroll
+                for (int i = 0; i < TB; ++i)
+                    xp[q][HLO + i] = o[i];
+            }
+        }
+        return;
+    }
 #pragma unroll
     for (int q = 0; q < CH / 2; ++q)
 #pragma unroll
@@ -1114,6 +1184,7 @@ struct ConvBwdParams {
     int batch, dim, L;
     int cg_log2;
     int ctiles, runs;   // warp tiles over channels, runs of steps over tokens
+    int across;         // a block's warps: over channels (else over runs)
     int steps;          // warp steps (token tiles) per run
     ConvView x, dy, dx;
     const float *weight, *bias;
@@ -1139,24 +1210,28 @@ __global__ void __launch_bounds__(128, 4) conv_bwd_kernel(const __grid_constant_
     constexpr int CH = conv_bwd_ch(XTOK, YTOK), TB = 16 / int(sizeof(T)), Q = CH / 2, H = W - 1;
     using XIO = BlockIO<T, XTOK, CH, TB, H>;
     using YIO = BlockIO<T, YTOK, CH, TB, 0>;
-    // what fits into 48 KB beside the taps
-    constexpr bool RING = (XIO::N * XIO::BYTES + YIO::N * YIO::BYTES) * 32 * 8 <= 46000;
+    // tiles staged: the next one too where 48 KB hold it beside the taps
+    constexpr int NS = (XIO::N * XIO::BYTES + YIO::N * YIO::BYTES) * 32 * 8 <= 46000 ? 2 : 1;
     __shared__ __align__(16) ConvTaps<W, 32 * CH> taps;
-    __shared__ typename XIO::Piece xring[RING ? 4 : 1][RING ? 2 : 1][RING ? XIO::N : 1][RING ? 32 : 1];
-    __shared__ typename YIO::Piece yring[RING ? 4 : 1][RING ? 2 : 1][RING ? YIO::N : 1][RING ? 32 : 1];
+    __shared__ typename XIO::Piece xring[4][NS][XIO::N][32];
+    __shared__ typename YIO::Piece yring[4][NS][YIO::N][32];
     const int lane = threadIdx.x & 31;
     const int ngr = 32 >> p.cg_log2;  // token blocks of a tile
     const int cg = lane & ((1 << p.cg_log2) - 1), tg = lane >> p.cg_log2;
-    // a block's warps take neighbouring runs of the same channels
-    const int ct = int(blockIdx.x % unsigned(p.ctiles));
-    const int run = int(blockIdx.x / unsigned(p.ctiles)) * 4 + int(threadIdx.x >> 5);
+    // a block's warps take neighbouring channels of one run or, where one warp
+    // takes as many channels as the taps' place holds, neighbouring runs
+    const int wp = int(threadIdx.x >> 5);
+    const int ctb = p.across ? (p.ctiles + 3) / 4 : p.ctiles;
+    const int ct = int(blockIdx.x % unsigned(ctb)) * (p.across ? 4 : 1) + (p.across ? wp : 0);
+    const int run = int(blockIdx.x / unsigned(ctb)) * (p.across ? 1 : 4) + (p.across ? 0 : wp);
     const int b = int(blockIdx.y);
-    const int cb = (ct << p.cg_log2) * CH, c0 = cb + cg * CH;
+    const int cb = (int(blockIdx.x % unsigned(ctb)) * (p.across ? 4 : 1) << p.cg_log2) * CH;
+    const int co = ((p.across ? wp << p.cg_log2 : 0) + cg) * CH, c0 = cb + co;
     const int tile = ngr * TB;
     const T *past = static_cast<const T *>(p.h0);
-    taps.stage(p.weight, p.bias, cb, CH << p.cg_log2, p.dim);
+    taps.stage(p.weight, p.bias, cb, (CH << p.cg_log2) * (p.across ? 4 : 1), p.dim);
     __syncthreads();
-    if (run >= p.runs)
+    if (run >= p.runs || ct >= p.ctiles)
         return;
     uint64_t dw[Q][W], db[Q];
     uint64_t head[Q][H];  // this block's first W-1 g of the tile done before
@@ -1182,7 +1257,7 @@ __global__ void __launch_bounds__(128, 4) conv_bwd_kernel(const __grid_constant_
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
                 uint64_t w[W], bias;
-                taps.read(w, bias, cg * CH + 2 * q);
+                taps.read(w, bias, co + 2 * q);
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     uint64_t e[W];
@@ -1200,77 +1275,62 @@ __global__ void __launch_bounds__(128, 4) conv_bwd_kernel(const __grid_constant_
     const auto start = [&](int step) {
         return int(min(first + int64_t(step) * tile + int64_t(tg) * TB, int64_t(p.L)));
     };
-    const auto staged = [&](int t0) {
-        return RING && XIO::inside(p.x, c0, t0, p.dim, p.L) && YIO::inside(p.dy, c0, t0, p.dim, p.L);
-    };
-    const int wp = RING ? int(threadIdx.x >> 5) : 0, ln = RING ? lane : 0;
     const auto fetch = [&](int step) {
-        if constexpr (RING) {
-            const int t0 = step >= 0 ? start(step) : p.L;
-            if (staged(t0)) {
-                XIO::each(p.x, b, c0, t0, [&](int i, const T *r) {
-                    cp_async_ca<XIO::BYTES>(&xring[wp][step & 1][i][ln], r);
-                });
-                YIO::each(p.dy, b, c0, t0, [&](int i, const T *r) {
-                    cp_async_ca<YIO::BYTES>(&yring[wp][step & 1][i][ln], r);
-                });
-            }
-            cp_async_commit();
+        if (step < 0)
+            return;
+        const int t0 = start(step);
+        typename XIO::Piece *xr = &xring[wp][step % NS][0][lane];
+        typename YIO::Piece *yr = &yring[wp][step % NS][0][lane];
+        if (XIO::inside(p.x, c0, t0, p.dim, p.L) && YIO::inside(p.dy, c0, t0, p.dim, p.L)) {
+            XIO::each(p.x, b, c0, t0,
+                      [&](int i, const T *r) { cp_async_ca<XIO::BYTES>(xr + i * 32, r); });
+            YIO::each(p.dy, b, c0, t0,
+                      [&](int i, const T *r) { cp_async_ca<YIO::BYTES>(yr + i * 32, r); });
+        } else {
+            // an edge, or rows without whole vectors (zeros behind the end)
+            pair_t<T> xp[Q][H + TB], yp[Q][TB];
+            load_block<T, XTOK, CH, TB, H>(xp, p.x, past, H, b, c0, t0, p.dim, p.L);
+            load_block<T, YTOK, CH, TB, 0>(yp, p.dy, nullptr, 0, b, c0, t0, p.dim, p.L);
+            XIO::give(xr, xp);
+            YIO::give(yr, yp);
         }
     };
-    fetch(p.steps - 1);
+    if (NS > 1) {
+        fetch(p.steps - 1);
+        cp_async_commit();
+    }
     for (int step = p.steps - 1; step >= 0; --step) {
-        fetch(step - 1);
+        fetch(NS > 1 ? step - 1 : step);
+        cp_async_commit();
         const int64_t tl = first + int64_t(step) * tile;  // the tile's first token
-        if (RING)
-            cp_async_wait<1>();
+        cp_async_wait<NS - 1>();
         if (tl >= p.L)
             continue;  // nothing there: g is zero (uniform over the warp)
         const int t0 = start(step);
-        pair_t<T> xp[Q][H + TB], yp[Q][TB];
-        if (RING && staged(t0)) {
-            typename XIO::Piece xw[XIO::N];
-            typename YIO::Piece yw[YIO::N];
-#pragma unroll
-            for (int i = 0; i < XIO::N; ++i)
-                xw[i] = xring[wp][step & (RING ? 1 : 0)][RING ? i : 0][ln];
-#pragma unroll
-            for (int i = 0; i < YIO::N; ++i)
-                yw[i] = yring[wp][step & (RING ? 1 : 0)][RING ? i : 0][ln];
-            XIO::unpack(xw, xp);
-            YIO::unpack(yw, yp);
-        } else if (t0 < p.L) {
-            load_block<T, XTOK, CH, TB, H>(xp, p.x, past, H, b, c0, t0, p.dim, p.L);
-            load_block<T, YTOK, CH, TB, 0>(yp, p.dy, nullptr, 0, b, c0, t0, p.dim, p.L);
-        } else {
-#pragma unroll
-            for (int q = 0; q < Q; ++q) {
-#pragma unroll
-                for (int i = 0; i < H + TB; ++i)
-                    xp[q][i] = 0;
-#pragma unroll
-                for (int i = 0; i < TB; ++i)
-                    yp[q][i] = 0;
-            }
-        }
+        const typename XIO::Piece *xr = &xring[wp][step % NS][0][lane];
+        const typename YIO::Piece *yr = &yring[wp][step % NS][0][lane];
+        pair_t<T> dp[Q][TB];
         const int src = ((tg + 1) & (ngr - 1)) * (32 / ngr) + cg;
         const bool tail = p.dlast && t0 + TB > p.L - H;
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             uint64_t w[W], bias, g[TB + H];
-            taps.read(w, bias, cg * CH + 2 * q);
+            taps.read(w, bias, co + 2 * q);
+            pair_t<T> xq[H + TB], yq[TB];
+            XIO::take(xr, q, xq);
+            YIO::take(yr, q, yq);
             with_flag(p.silu, [&](auto silu) {
                 uint64_t e[W];
 #pragma unroll
                 for (int k = 0; k < H; ++k)
-                    e[k + 1] = PairOf<T>::f2(xp[q][k]);
+                    e[k + 1] = PairOf<T>::f2(xq[k]);
 #pragma unroll
                 for (int i = 0; i < TB; ++i) {
 #pragma unroll
                     for (int k = 0; k < H; ++k)
                         e[k] = e[k + 1];
-                    e[H] = PairOf<T>::f2(xp[q][H + i]);
-                    g[i] = PairOf<T>::f2(yp[q][i]);
+                    e[H] = PairOf<T>::f2(xq[H + i]);
+                    g[i] = PairOf<T>::f2(yq[i]);
                     if (decltype(silu)::value)
                         g[i] = silu_grad2<T>(tap_sum<W>(w, e, bias), g[i]);
 #pragma unroll
@@ -1330,10 +1390,10 @@ __global__ void __launch_bounds__(128, 4) conv_bwd_kernel(const __grid_constant_
             }
 #pragma unroll
             for (int i = 0; i < TB; ++i)
-                yp[q][i] = PairOf<T>::round(g[i]);  // dx, in place of dy
+                dp[q][i] = PairOf<T>::round(g[i]);
         }
         if (t0 < p.L)
-            store_block<T, XTOK, CH, TB>(yp, p.dx, b, c0, t0, p.dim, p.L);
+            store_block<T, XTOK, CH, TB>(dp, p.dx, b, c0, t0, p.dim, p.L);
     }
     // the run's sums over the warp's token blocks
     for (int off = 16; off >= (1 << p.cg_log2); off >>= 1)

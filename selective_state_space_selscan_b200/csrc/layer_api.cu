@@ -400,11 +400,23 @@ extern "C" selscan_status selscan_conv_bwd(const selscan_tensor *x, const selsca
     p.ctiles = int((cblocks + (1 << p.cg_log2) - 1) >> p.cg_log2);
     const int ngr = 32 >> p.cg_log2;
     const int64_t tiles = (tblocks + ngr - 1) / ngr;
-    // runs: enough warps for every SM, and as few steps above a run as that allows
-    const int64_t want = std::max<int64_t>(1, 32ll * di->sm_count / (int64_t(p.ctiles) * batch));
-    int64_t runs = std::min(tiles, want);
+    // Runs: the fewest steps in sequence, with whole waves of blocks (four per
+    // SM) and about half a step for a run's start and the W-1 tokens above it.
+    p.across = p.cg_log2 <= 3;
+    const int64_t per_run = p.across ? (p.ctiles + 3) / 4 * batch : int64_t(p.ctiles) * batch;
+    const auto blocks_of = [&](int64_t r) { return p.across ? per_run * r : per_run * ((r + 3) / 4); };
+    double best = 1e300;
+    int64_t runs = 1;
+    for (int64_t r = 1; r <= std::min<int64_t>(tiles, 256); ++r) {
+        const int64_t steps = (tiles + r - 1) / r, rr = (tiles + steps - 1) / steps;
+        const double waves = double((blocks_of(rr) + 4 * di->sm_count - 1) / (4 * di->sm_count));
+        const double t = waves * (double(steps) + 0.5);
+        if (t < best * 0.999) {
+            best = t;
+            runs = rr;
+        }
+    }
     p.steps = int((tiles + runs - 1) / runs);
-    runs = (tiles + p.steps - 1) / p.steps;
     p.runs = int(runs);
     p.x = view_of(x, xt);
     p.dy = view_of(dy, yt);
@@ -415,7 +427,7 @@ extern "C" selscan_status selscan_conv_bwd(const selscan_tensor *x, const selsca
     p.dlast = opt_data(dlast);
     p.dh0 = dh0 ? dh0->data : nullptr;
     p.silu = silu ? 1 : 0;
-    const int64_t gx = (runs + 3) / 4 * p.ctiles;
+    const int64_t gx = blocks_of(runs) / batch;
     const int64_t rows = batch * runs;
     if (gx > 0x7fffffffll || rows > 0x7fffffffll || dim * (W + 1) > 0x7fffffffll)
         return SELSCAN_ERR_UNSUPPORTED;
