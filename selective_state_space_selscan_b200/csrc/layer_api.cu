@@ -390,26 +390,26 @@ extern "C" selscan_status selscan_conv_bwd(const selscan_tensor *x, const selsca
     if ((st = device_setup(&dev, &di)) != SELSCAN_OK)
         return st;
     const bool xt = token_major(x), yt = token_major(dy);
-    const int64_t ch = conv_bwd_ch(xt, yt), blk = 16 / int64_t(elem_size(dt));
+    const int64_t ch = kConvBwdCh, blk = 16 / int64_t(elem_size(dt));
     const int64_t cblocks = (dim + ch - 1) / ch, tblocks = (L + blk - 1) / blk;
     ConvBwdParams p{};
     p.batch = int(batch);
     p.dim = int(dim);
     p.L = int(L);
-    p.cg_log2 = channel_blocks_log2(xt ? (yt ? 5 : 3) : (yt ? 3 : 0), cblocks, tblocks);
+    p.cg_log2 = channel_blocks_log2(xt ? (yt ? 5 : 4) : (yt ? 4 : 0), cblocks, tblocks);
     p.ctiles = int((cblocks + (1 << p.cg_log2) - 1) >> p.cg_log2);
     const int ngr = 32 >> p.cg_log2;
     const int64_t tiles = (tblocks + ngr - 1) / ngr;
-    // Runs: the fewest steps in sequence, with whole waves of blocks (four per
+    // Runs: the fewest steps in sequence, with whole waves of blocks (five per
     // SM) and about half a step for a run's start and the W-1 tokens above it.
-    p.across = p.cg_log2 <= 3;
+    p.across = p.cg_log2 <= 4;
     const int64_t per_run = p.across ? (p.ctiles + 3) / 4 * batch : int64_t(p.ctiles) * batch;
     const auto blocks_of = [&](int64_t r) { return p.across ? per_run * r : per_run * ((r + 3) / 4); };
     double best = 1e300;
     int64_t runs = 1;
     for (int64_t r = 1; r <= std::min<int64_t>(tiles, 256); ++r) {
         const int64_t steps = (tiles + r - 1) / r, rr = (tiles + steps - 1) / steps;
-        const double waves = double((blocks_of(rr) + 4 * di->sm_count - 1) / (4 * di->sm_count));
+        const double waves = double((blocks_of(rr) + 5 * di->sm_count - 1) / (5 * di->sm_count));
         const double t = waves * (double(steps) + 0.5);
         if (t < best * 0.999) {
             best = t;
