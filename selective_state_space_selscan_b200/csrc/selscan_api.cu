@@ -93,10 +93,13 @@ selscan_status device_setup(int *dev_out, DeviceInfo **info_out)
     return SELSCAN_OK;
 }
 
-// The pool is the library's own on the current device.  Its release threshold keeps freed memory mapped: the device's
-// default pool hands memory back to the driver at every synchronisation, so
-// the next call would map the backward checkpoints (hundreds of MB) again.
-// selscan_release_scratch() trims the pools.
+// The pool is the library's own on the current device.  Its release threshold
+// keeps freed memory mapped: the device's default pool hands memory back to
+// the driver at every synchronisation, so the next call would map the backward
+// checkpoints (hundreds of MB) again.  selscan_release_scratch() trims the
+// pools.  The first call on a device may come inside a stream capture:
+// creating a pool is no work of the stream's, but only the relaxed capture
+// mode lets it through.
 cudaError_t scratch_alloc(void **p, size_t bytes, cudaStream_t stream)
 {
     int dev = 0;
@@ -115,14 +118,17 @@ cudaError_t scratch_alloc(void **p, size_t bytes, cudaStream_t stream)
             props.location.type = cudaMemLocationTypeDevice;
             props.location.id = dev;
             cudaMemPool_t np = nullptr;
-            if ((e = cudaMemPoolCreate(&np, &props)) != cudaSuccess)
+            cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+            if ((e = cudaThreadExchangeStreamCaptureMode(&mode)) != cudaSuccess)
                 return e;
             uint64_t keep = UINT64_MAX;
-            if ((e = cudaMemPoolSetAttribute(np, cudaMemPoolAttrReleaseThreshold, &keep)) !=
-                cudaSuccess) {
+            if ((e = cudaMemPoolCreate(&np, &props)) == cudaSuccess &&
+                (e = cudaMemPoolSetAttribute(np, cudaMemPoolAttrReleaseThreshold, &keep)) !=
+                    cudaSuccess)
                 cudaMemPoolDestroy(np);
+            cudaThreadExchangeStreamCaptureMode(&mode);  // back to what it was
+            if (e != cudaSuccess)
                 return e;
-            }
             g_pool[dev] = np;
         }
         pool = g_pool[dev];

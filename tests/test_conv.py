@@ -294,6 +294,26 @@ def test_conv_offsets_past_32_bits():
     ss.check()
 
 
+def test_conv_sizes_of_every_launch_form():
+    """Sizes at which the kernels take another split: channels that fill a
+    warp, part of it, or several; runs of one tile, of many, of a part."""
+    import selective_state_space_selscan_b200 as ss
+    rng = np.random.default_rng(16)
+    for b, D, L in ((1, 2, 3000), (1, 1024, 9), (2, 260, 515), (1, 32, 4100), (5, 72, 64)):
+        for dtype in ("f32", "bf16"):
+            for layout in ("channels", "tokens", "half"):
+                x, w, dy = rnd(rng, b, D, L, dtype=dtype), rnd(rng, D, 4), rnd(rng, b, D, L, dtype=dtype)
+                ref, last, size = plain_layer.conv(x, w)
+                y, st = ss.selscan_conv(dev(x, dtype, layout), dev(w))
+                near(y, ref, half_step(dtype) * np.abs(ref) + F32 * (size + np.abs(ref)), (b, D, L))
+                gr = plain_layer.conv_grads(x, w, dy)
+                g = ss.selscan_conv_bwd(dev(x, dtype, layout), dev(w), dev(dy, dtype))
+                ss.check()
+                near(g["dx"], gr["dx"], half_step(dtype) * np.abs(gr["dx"]) + 2 * F32 * gr["dxsize"])
+                near(g["dweight"], gr["dweight"],
+                     ((b * L + 16) * 2.0 ** -24 + 2 * F32) * gr["dwsize"])
+
+
 # ------------------------------------------------------------ single tokens
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("batch,D", [(1, 64), (3, 40), (5, 7), (33, 1), (2, 1030), (300, 16)])

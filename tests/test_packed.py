@@ -438,6 +438,35 @@ def test_step_refuses_slots_on_the_device():
 
 
 # ------------------------------------------------------- as they are used
+def test_many_sequences():
+    """More sequences than one probe of a warp sees (32) and more than its
+    square, single tokens among them."""
+    import selective_state_space_selscan_b200 as ss
+    rng = np.random.default_rng(36)
+    D = 24
+    for count in (33, 200, 1500):
+        lens = rng.integers(0, 4, count)
+        lens[rng.integers(0, count, 3)] = 90
+        pk = Packed(rng, lens, tail=2)
+        inp = scan_inputs(rng, pk.tokens, D, "f32")
+        x, w = inp["u"], rnd(rng, D, 4)
+        state0, cst0 = rnd(rng, pk.count, D, N), rnd(rng, pk.count, D, 3)
+        y0 = np.zeros((pk.tokens, D), np.float32)
+        y_ref, s_ref = scan_reference(pk, inp, state0, y0)
+        state, out = dev(state0), dev(y0)
+        scan_call(pk, inp, state, out, "f32")
+        cst, yc = dev(cst0), dev(y0)
+        ss.selscan_conv_packed(cst, dev(x), dev(w), *pk.args(), seen=i32(pk.seen), out=yc)
+        ss.check()
+        assert rel(host(out), y_ref) <= 1e-5 and rel(host(state), s_ref) <= 1e-5
+        c_ref, st_ref = np.zeros_like(y_ref), cst0.astype(np.float64)
+        for i, rows, slot in pk.each():
+            y, st_ref[slot], _ = plain_layer.conv(x[rows].T, w, None, True,
+                                                  st_ref[slot] if pk.seen[i] else None)
+            c_ref[rows] = y.T
+        assert rel(host(yc), c_ref) <= 1e-5 and np.array_equal(host(cst), st_ref)
+
+
 def test_packed_calls_in_two_graphs():
     """Two captured graphs of the same calls (each with its own scratch in the
     capture), replayed in turn with new inputs, equal the eager calls."""
@@ -482,6 +511,100 @@ def test_packed_calls_in_two_graphs():
             assert torch.equal(y, y2) and torch.equal(v, v2)
             assert torch.equal(cache, c2) and torch.equal(conv, k2)
     ss.check()
+
+
+@pytest.mark.parametrize("which", ["conv_bwd", "packed", "step"])
+def test_first_call_inside_a_capture(which):
+    """In a fresh process the library's first call on a device, which makes
+    its scratch pool, may be a captured one."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = f"""
+import sys
+sys.path.insert(0, {root!r})
+import torch
+import selective_state_space_selscan_b200 as ss
+r = lambda *s: torch.randn(*s, device="cuda")
+i = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+x, w, A, cache, bc = r(2, 64, 40), r(64, 4), -r(64, 16).abs(), r(3, 64, 16), r(2000, 16)
+t, start, slots, row = r(2000, 64), i(0, 1900, 2000), i(0, 2), r(2, 64)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    if {which!r} == "conv_bwd":
+        ss.selscan_conv_bwd(x, w, x)
+    elif {which!r} == "packed":
+        ss.selscan_fwd_packed(cache, t, t, A, bc, bc, start, slots)
+    else:
+        ss.selscan_step(cache, row, row, A, bc[:2], bc[:2], slots=slots)
+g.replay()
+ss.check()
+print("captured")
+"""
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert "captured" in out.stdout, out.stdout + out.stderr
+
+
+def test_rows_of_no_sequence_may_hold_anything():
+    """NaN in the rows behind the last sequence and before the first, in slots
+    that no sequence owns, and in the state of a sequence that starts from
+    zero, reaches nothing."""
+    import torch
+    import selective_state_space_selscan_b200 as ss
+    rng = np.random.default_rng(34)
+    D = 136
+    for dtype in ("f32", "bf16"):
+        for lens in ([5, 0, 40], [0, 0], [300, 1]):
+            pk = Packed(rng, lens, tail=9, lead=6)
+            pk.seen = np.array([0, 3, 0][:len(lens)])
+            inp = scan_inputs(rng, pk.tokens, D, dtype)
+            state0 = rnd(rng, pk.count, D, N)
+            y0 = rnd(rng, pk.tokens, D, dtype=dtype)
+            w = rnd(rng, D, 4)
+            cst0 = rnd(rng, pk.count, D, 3, dtype=dtype)
+            results = []
+            for bad in (0.0, np.nan):
+                x = {k: v.copy() for k, v in inp.items()}
+                for k in ("u", "delta", "z", "B", "C"):
+                    x[k][~pk.owned] = bad
+                st, cst = state0.copy(), cst0.copy()
+                loose = [s for s in range(pk.count)
+                         if s not in pk.slots or pk.seen[list(pk.slots).index(s)] == 0]
+                st[loose] = bad
+                cst[loose] = bad
+                state, conv, out, yc = dev(st), dev(cst, dtype), dev(y0, dtype), dev(y0, dtype)
+                scan_call(pk, x, state, out, dtype)
+                ss.selscan_conv_packed(conv, dev(x["u"], dtype), dev(w), *pk.args(),
+                                       seen=i32(pk.seen), out=yc)
+                ss.check()
+                at = torch.from_numpy(pk.slots.astype(np.int64)).cuda()
+                results.append((out, yc, state[at], conv[at]))
+            for a, b in zip(*results):
+                assert torch.equal(a, b)
+
+
+def test_no_rows_at_all():
+    """Sequences without rows: states stay, or are zeroed where nothing was
+    seen."""
+    import torch
+    import selective_state_space_selscan_b200 as ss
+    rng = np.random.default_rng(35)
+    D = 40
+    for dtype in ("f32", "bf16"):
+        empty = dev(np.zeros((0, D), np.float32), dtype)
+        bc = dev(np.zeros((0, N), np.float32), dtype)
+        state0, conv0 = rnd(rng, 4, D, N), rnd(rng, 4, D, 3, dtype=dtype)
+        state, conv = dev(state0), dev(conv0, dtype)
+        start, slots, seen = i32([0, 0, 0]), i32([2, 0]), i32([0, 4])
+        y = ss.selscan_fwd_packed(state, empty, empty, dev(-np.ones((D, N), np.float32)), bc, bc,
+                                  start, slots, seen=seen)
+        yc = ss.selscan_conv_packed(conv, empty, dev(rnd(rng, D, 4)), start, slots, seen=seen)
+        ss.check()
+        assert y.shape == yc.shape == (0, D)
+        state0[2], conv0[2] = 0, 0
+        assert np.array_equal(host(state), state0) and np.array_equal(host(conv), conv0)
 
 
 def test_serving_loop_equals_the_whole_sequences():
