@@ -1,10 +1,14 @@
 """libselscan: the selective scan (S6) and the short causal convolution in
 front of it, for NVIDIA B200 (sm_100a).
 
-This package is a thin ctypes binding over the C ABI in ``include/selscan.h``
+This package is a thin binding over the C ABI in ``include/selscan.h``
 (built in-tree as ``libselscan.so`` by ``build.py``).  It only marshals
 arguments: every step of the scan runs in the library's CUDA kernels.  There
 is no CPU fallback; if the shared library is missing the functions raise.
+The dense scan goes through ctypes; the entry points that small calls use
+(single tokens, packed prompts, the convolution) go through ``_bind.so``
+(``csrc/bind.cpp``), which reads the tensors in C++, or through ctypes where
+that is not built.
 
 PyTorch is used for device memory and streams only: tensors are passed by
 pointer, shape and strides.
@@ -221,37 +225,73 @@ def _descs(*tensors):
     return dev, out
 
 
-def _launch(name, dev, stream, *args):
-    """Call an entry point with the tensors' device current, on ``stream`` (by
-    default that device's current stream)."""
-    import torch
-    if stream is None:
-        # the handle alone: a Stream object costs more than a small kernel
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        handle = raw(dev) if raw else torch.cuda.current_stream(dev).cuda_stream
-    elif stream.device_index != dev:
-        raise ValueError(f"{name}: the stream is on cuda:{stream.device_index}, the tensors "
-                         f"on cuda:{dev}")
+# entry points of _bind.so, by number, and where their numbers (flags, headdim)
+# stand among the arguments
+_ENTRY = {name: i for i, name in enumerate((
+    "selscan_step_slots", "selscan_step_scalarA_slots", "selscan_fwd_packed", "selscan_conv",
+    "selscan_conv_bwd", "selscan_conv_step", "selscan_conv_packed"))}
+_bound = None      # its call(entry, stream handle or None, arguments...)
+_bound_empty = None  # its empty(like, fp32, sizes...)
+
+
+def _binding():
+    """_bind.so's call, or False where it is not built for this torch."""
+    global _bound, _bound_empty
+    if _bound is None:
+        import torch  # noqa: F401  (its libraries come first)
+        lib()
+        try:
+            from . import _bind
+            _bound, _bound_empty = _bind.call, _bind.empty
+        except ImportError:
+            _bound = False
+    return _bound
+
+
+def _call(name, stream, *args):
+    """Call an entry point on tensors (None: absent) and numbers, with the
+    tensors' device current, on ``stream`` (by default that device's current
+    stream)."""
+    call = _bound if _bound is not None else _binding()
+    if call:
+        handle = None
+        if stream is not None:
+            if args[0].is_cuda and args[0].get_device() != stream.device_index:
+                raise ValueError(f"{name}: the stream is on cuda:{stream.device_index}, the "
+                                 f"tensors on {args[0].device}")
+            handle = stream.cuda_stream
+        rc = call(_ENTRY[name], handle, *args)
     else:
-        handle = stream.cuda_stream
-    f = getattr(lib(), name)
-    if torch.cuda.current_device() == dev:
-        rc = f(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            rc = f(*args, handle)
+        rc = _call_ctypes(name, stream, *args)
     if rc != 0:
         raise SelscanError(rc, name)
 
 
-def _empty(stream, like, shape, dtype=None):
-    """An output on the stream that writes it, so that the allocator does not
-    hand out memory that another stream still uses."""
-    if stream is None:
-        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+def _call_ctypes(name, stream, *args):
     import torch
-    with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+    dev, descs = _descs(*[a for a in args if not isinstance(a, int)])
+    it = iter(descs)
+    args = [a if isinstance(a, int) else next(it) for a in args]
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"{name}: the stream is on cuda:{stream.device_index}, the tensors "
+                         f"on cuda:{dev}")
+    with torch.cuda.device(dev):
+        return getattr(lib(), name)(*args, stream.cuda_stream)
+
+
+def _empty(stream, like, shape, dtype=None):
+    """A contiguous output like ``like`` (or fp32, the only ``dtype``), on the
+    stream that writes it, so that the allocator does not hand out memory that
+    another stream still uses."""
+    if stream is not None:
+        import torch
+        with torch.cuda.stream(stream):
+            return like.new_empty(shape, dtype=dtype)
+    if (_bound if _bound is not None else _binding()) and 1 <= len(shape) <= 4:
+        return _bound_empty(like, dtype is not None, *shape)
+    return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
 
 
 def _stream_handle(stream):
@@ -359,8 +399,8 @@ def selscan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=None,
     import torch
     if slots is not None:
         y = out if out is not None else _empty(stream, u, u.shape)
-        dev, d = _descs(state, slots, u, delta, delta_bias, A, B, C, D, z, y)
-        _launch("selscan_step_slots", dev, stream, *d[:5], int(bool(delta_softplus)), *d[5:])
+        _call("selscan_step_slots", stream, state, slots, u, delta, delta_bias,
+              int(bool(delta_softplus)), A, B, C, D, z, y)
         return y
     y = out if out is not None else torch.empty(u.shape, dtype=u.dtype, device=u.device)
     d = [describe(t) for t in (state, u, delta, delta_bias, A, B, C, D, z, y)]
@@ -383,9 +423,8 @@ def selscan_step_scalarA(state, x, dt, A, B, C, headdim, D=None, z=None, dt_bias
     import torch
     if slots is not None:
         y = out if out is not None else _empty(stream, x, x.shape)
-        dev, d = _descs(state, slots, x, dt, dt_bias, A, B, C, D, z, y)
-        _launch("selscan_step_scalarA_slots", dev, stream, *d[:5], int(bool(dt_softplus)),
-                *d[5:10], int(headdim), d[10])
+        _call("selscan_step_scalarA_slots", stream, state, slots, x, dt, dt_bias,
+              int(bool(dt_softplus)), A, B, C, D, z, int(headdim), y)
         return y
     y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
     d = [describe(t) for t in (state, x, dt, dt_bias, A, B, C, D, z, y)]
@@ -489,8 +528,8 @@ def selscan_fwd_packed(state, u, delta, A, B, C, start, slots, D=None, z=None,
     of ``out``, and rows of no sequence, are left as they were.  Returns y
     (tokens, D)."""
     y = out if out is not None else _empty(stream, u, u.shape)
-    dev, d = _descs(state, u, delta, delta_bias, A, B, C, D, z, start, slots, seen, y)
-    _launch("selscan_fwd_packed", dev, stream, *d[:4], int(bool(delta_softplus)), *d[4:])
+    _call("selscan_fwd_packed", stream, state, u, delta, delta_bias, int(bool(delta_softplus)),
+          A, B, C, D, z, start, slots, seen, y)
     return y
 
 
@@ -508,8 +547,7 @@ def selscan_conv(x, weight, bias=None, silu=True, h0=None, out=None, last_state=
     y = out if out is not None else _empty(stream, x, x.shape)
     if last_state is None and return_last_state:
         last_state = _empty(stream, x, (x.shape[0], x.shape[1], weight.shape[1] - 1))
-    dev, d = _descs(x, weight, bias, h0, y, last_state)
-    _launch("selscan_conv", dev, stream, *d[:3], int(bool(silu)), *d[3:])
+    _call("selscan_conv", stream, x, weight, bias, int(bool(silu)), h0, y, last_state)
     return y, last_state
 
 
@@ -531,8 +569,8 @@ def selscan_conv_bwd(x, weight, dy, bias=None, silu=True, h0=None, dlast=None, n
            "dbias": _empty(stream, x, (dim,), f32) if bias is not None else None,
            "dh0": _empty(stream, x, (batch, dim, weight.shape[1] - 1))
            if (h0 is not None or need_dh0) else None}
-    dev, d = _descs(x, weight, bias, h0, dy, dlast, dx, out["dweight"], out["dbias"], out["dh0"])
-    _launch("selscan_conv_bwd", dev, stream, *d[:3], int(bool(silu)), *d[3:])
+    _call("selscan_conv_bwd", stream, x, weight, bias, int(bool(silu)), h0, dy, dlast, dx,
+          out["dweight"], out["dbias"], out["dh0"])
     return out
 
 
@@ -541,8 +579,7 @@ def selscan_conv_step(state, x, weight, bias=None, silu=True, slots=None, out=No
     is updated in place.  x: (batch, D) (any strides).  With ``slots`` the state
     is a cache (count, D, W-1), as in selscan_step.  Returns y (batch, D)."""
     y = out if out is not None else _empty(stream, x, x.shape)
-    dev, d = _descs(state, slots, x, weight, bias, y)
-    _launch("selscan_conv_step", dev, stream, *d[:5], int(bool(silu)), d[5])
+    _call("selscan_conv_step", stream, state, slots, x, weight, bias, int(bool(silu)), y)
     return y
 
 
@@ -553,8 +590,8 @@ def selscan_conv_packed(state, x, weight, start, slots, bias=None, silu=True, se
     (tokens, D), channel stride 1; start, slots and seen as in
     selscan_fwd_packed.  Returns y (tokens, D)."""
     y = out if out is not None else _empty(stream, x, x.shape)
-    dev, d = _descs(state, x, weight, bias, start, slots, seen, y)
-    _launch("selscan_conv_packed", dev, stream, *d[:4], int(bool(silu)), *d[4:])
+    _call("selscan_conv_packed", stream, state, x, weight, bias, int(bool(silu)), start, slots,
+          seen, y)
     return y
 
 

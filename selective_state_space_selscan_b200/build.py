@@ -14,6 +14,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libselscan.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("selscan_api.cu", "layer_api.cu")]
+BIND = os.path.join(PKG, "_bind.so")
+BIND_SRC = os.path.join(CSRC, "bind.cpp")
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC)
                   if f.endswith((".cuh", ".h"))] + [
     os.path.join(ROOT, "include", f) for f in os.listdir(os.path.join(ROOT, "include"))
@@ -60,6 +62,35 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     return LIB
 
 
+def build_bind(force: bool = False, verbose: bool = False) -> str:
+    """Compile _bind.so (tensors to the C ABI, csrc/bind.cpp) against the
+    installed torch, unless it is newer than its sources."""
+    header = os.path.join(ROOT, "include", "selscan.h")
+    if (not force and os.path.exists(BIND)
+            and os.path.getmtime(BIND) >= max(os.path.getmtime(p) for p in (BIND_SRC, header))):
+        return BIND
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(ROOT, "include"), os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"],
+           os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")]
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{p}" for p in inc], "-o", tmp, BIND_SRC, "-L", PKG, "-l:libselscan.so",
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+           "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.check_call(cmd)
+    os.replace(tmp, BIND)
+    return BIND
+
+
 if __name__ == "__main__":
     build(force="--force" in sys.argv, verbose=True,
           extra=["-Xptxas", "-v"] if "--ptxas-v" in sys.argv else [])
+    build_bind(force="--force" in sys.argv, verbose=True)

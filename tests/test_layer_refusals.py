@@ -208,8 +208,12 @@ def test_nothing_to_do_is_accepted_without_a_device():
                       slots=t((0,), I32)) == 0
 
 
-def test_host_tensors_are_refused():
+@pytest.mark.parametrize("bound", [True, False])
+def test_host_tensors_are_refused(bound, monkeypatch):
+    """By the C++ binding and by the ctypes one."""
     import torch
+    assert ss._binding(), "_bind.so is not built"
+    monkeypatch.setattr(ss, "_bound", ss._binding() if bound else False)
     x = torch.zeros(2, 24, 40)
     w, s = torch.zeros(24, 4), torch.zeros(2, 24, 3)
     i = torch.zeros(3, dtype=torch.int32)
@@ -227,3 +231,18 @@ def test_host_tensors_are_refused():
 
 def test_index_status_has_a_name():
     assert C["SELSCAN_ERR_INDEX"] == 9 and "slot" in ss._strerror(9)
+
+
+def test_binding_checks_its_arguments():
+    import torch
+    call = ss._binding()
+    with pytest.raises(TypeError, match="torch tensors"):
+        call(ss._ENTRY["selscan_conv"], None, "x", None, None, 1, None, None, None)
+    with pytest.raises(TypeError, match="too few"):
+        call(ss._ENTRY["selscan_conv"], None, None, None)
+    with pytest.raises(ValueError, match="entry point"):
+        call(99, None)
+    with pytest.raises(TypeError):
+        call(ss._ENTRY["selscan_conv"], None, None, None, None, "silu", None, None, None)
+    assert call(ss._ENTRY["selscan_conv"], None, None, None, None, 1, None, None, None) == \
+        C["SELSCAN_ERR_NULL"]

@@ -513,6 +513,42 @@ def test_packed_calls_in_two_graphs():
     ss.check()
 
 
+def test_both_bindings_make_the_same_calls(monkeypatch):
+    """The C++ binding and the ctypes one, on every entry point they share."""
+    import torch
+    import selective_state_space_selscan_b200 as ss
+    rng = np.random.default_rng(37)
+    D = 64
+    pk = Packed(rng, [9, 70, 1])
+    inp = scan_inputs(rng, pk.tokens, D, "bf16")
+    x, w, b = dev(rnd(rng, 2, D, 50)), dev(rnd(rng, D, 4)), dev(rnd(rng, D))
+    h0, tok, bc = dev(rnd(rng, 2, D, 3)), dev(rnd(rng, 2, D)), dev(rnd(rng, 2, N))
+    dt = dev(rnd(rng, 2, 1))
+    bc128 = dev(rnd(rng, 2, 128))
+    assert ss._binding(), "_bind.so is not built"
+    results = []
+    for bind in (ss._binding(), False):
+        monkeypatch.setattr(ss, "_bound", bind)
+        rng = np.random.default_rng(38)
+        state, conv = dev(rnd(rng, pk.count, D, N)), dev(rnd(rng, pk.count, D, 3))
+        scal = dev(rnd(rng, 4, 1, 64, 128))
+        out = [scan_call(pk, inp, state, None, "bf16"), *ss.selscan_conv(x, w, bias=b, h0=h0)]
+        g = ss.selscan_conv_bwd(x, w, x, bias=b, h0=h0, dlast=h0)
+        out += [g[k] for k in ("dx", "dweight", "dbias", "dh0")]
+        out.append(ss.selscan_conv_packed(conv, dev(inp["u"]), w, *pk.args(), bias=b,
+                                          seen=i32(pk.seen)))
+        out.append(ss.selscan_conv_step(conv, tok, w, slots=i32([1, 0]),
+                                        stream=torch.cuda.current_stream()))
+        out.append(ss.selscan_step(state, tok, tok, dev(inp["A"]), bc, bc, D=b, slots=i32([0, 2])))
+        out.append(ss.selscan_step_scalarA(scal, tok, dt, -b[:1].abs(), bc128, bc128, 64, D=b[:1],
+                                           z=tok, dt_bias=b[:1], dt_softplus=True,
+                                           slots=i32([3, 1])))
+        ss.check()
+        results.append(out + [state, conv, scal])
+    for a, c in zip(*results):
+        assert torch.equal(a, c)
+
+
 @pytest.mark.parametrize("which", ["conv_bwd", "packed", "step"])
 def test_first_call_inside_a_capture(which):
     """In a fresh process the library's first call on a device, which makes
