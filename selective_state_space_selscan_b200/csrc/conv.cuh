@@ -1004,7 +1004,7 @@ __device__ __forceinline__ void packed_head(const PackedSeq &q, int c0, int dim,
 }
 
 template <typename T, int W, bool VEC>
-__global__ void __launch_bounds__(128, 4) conv_packed_kernel(const __grid_constant__ ConvPackedParams p)
+__global__ void __launch_bounds__(128, 3) conv_packed_kernel(const __grid_constant__ ConvPackedParams p)
 {
     constexpr int CH = VEC ? 16 / int(sizeof(T)) : 4, H = W - 1;
     __shared__ __align__(16) ConvTaps<W, 32 * CH> taps;
