@@ -177,7 +177,7 @@ PackedPlan packed_plan(int64_t tokens, int64_t seqs, int64_t dim, int64_t sms)
     };
     // a few short sequences: one segment each, one launch
     const int64_t seg4 =
-        tokens <= 512 && tokens <= 64 * seqs ? tokens + 1 : seg_of(warps4, 28 * sms);
+        tokens <= 512 && tokens <= 64 * seqs ? tokens + 1 : seg_of(warps4, 44 * sms);
     PackedPlan plan;
     plan.lanes = g_dbg_packed_lanes ? g_dbg_packed_lanes
                                     : (tokens > 2 * seqs * seg4 && seg4 > 64 ? 1 : 4);
