@@ -16,6 +16,14 @@
 // row (channels contiguous) and of a channels-first row (time contiguous)
 // both are whole vectors of the block: a token-major input is turned into a
 // channels-first output in registers.  Sums are fp32.
+//
+// What bounds them is HBM in the end (4 bytes per element forward, 6 backward,
+// 16 per channel and row for single tokens, in bf16), and on the way to it the
+// instructions per element (about 14 forward, 38 backward) and the loads in
+// flight.  Measured, bf16, four taps, SiLU: forward 4 x 5120 x 4096, token-major
+// in, channels-first out, 72 us (4.66 TB/s); packed 8192 x 2560 21.9 us (3.9
+// TB/s); backward 8 x 2560 x 2048 80 us (3.1 TB/s, 5 us of it the sum of the
+// runs); single tokens 1024 x 5120 18.0 us (4.7 TB/s).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -520,7 +528,8 @@ __device__ __forceinline__ T conv_tail(const T *x, int64_t st, int L, const T *p
 
 // A thread owns CH channels x TB tokens (16 bytes of either layout); a block
 // of four warps holds four neighbouring token tiles, so that the W-1 rows
-// that a tile reads from the tile before it come from L1.
+// that a tile reads from the tile before it come from L1.  Five blocks per SM:
+// 72 us for 4 x 5120 x 4096 bf16 (four 77, six, with 80 registers, 86).
 template <typename T, int W, bool XTOK, bool YTOK>
 __global__ void __launch_bounds__(128, 5) conv_fwd_kernel(const __grid_constant__ ConvParams p)
 {

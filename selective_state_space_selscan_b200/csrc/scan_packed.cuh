@@ -11,7 +11,7 @@
 // yet), which is left as the state after the sequence's last token.
 //
 // Work split.  A unit is a segment of at most seg_len tokens of one sequence
-// times kSpCT channels, one thread per channel with its 16 states in registers.
+// times 64 channels, two channels per thread with their states in registers.
 // The lengths are on the device, so the grid holds an upper bound of units,
 // tokens / seg_len + seqs, and a block finds its sequence by searching the
 // map i -> start[i] / seg_len + i, whose steps leave room for every
@@ -20,6 +20,23 @@
 // scans each from zero for its end state E and its sum of step sizes, a small
 // kernel folds these along the sequence (h <- exp(A sum delta) h + E), and
 // the output pass starts each segment from its folded state.
+//
+// What bounds it.  Not HBM (8 bytes per element and pass): a token of a channel
+// takes 16 decays, 16 inputs, 16 updates and 16 output products.  With a
+// general A the 16 exponentials alone hold the special-function unit for 128 of
+// an SM partition's cycles per 32 channels and token (21 with the step size and
+// the gate: 168); with A[n] = (n+1) A[0] the packed products hold the FMA pipe
+// for about 105 (a packed FMA of three different register pairs issues every
+// third cycle, a packed multiply every second, both measured; scalar FMAs in
+// their place were 2 % (outputs) to 20 % (updates) slower).  Measured, bf16
+// with gate: 131072 x 2048 in one prompt, A[n] = (n+1) A[0], 1.87 ms (pass 1
+// 0.75, output pass 1.15 = 157 cycles); 16384 x 2048 in 32 prompts of
+// log-normal lengths, general A, 0.38 ms; of which 0.13 ms are the first pass.
+// Tried and dropped: two of eight pairs of exponentials as polynomials on the
+// FMA pipe (10 to 13 instructions per pair instead of 2: issue-bound, 441
+// against 408 us), two lanes per channel (414 against 393 us), one channel per
+// thread (shared-memory bandwidth, 128 cycles for B and C alone), three staged
+// chunks with the outputs leaving through them (fewer blocks per SM).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -152,9 +169,10 @@ __device__ __forceinline__ uint64_t gate_pair(uint64_t z)
 // lanes share them, 16 / LPC states each:
 //  1: least work per token (the powers of the POW form are one running
 //     product);
-//  2, 4: a token takes a half, a quarter of the time, so that sequences need
-//     not be cut into segments to fill the GPU.  Of four tokens the lanes
-//     prepare two or one each (step sizes, gate) and exchange.
+//  4: a token takes about a quarter of the time, so that most sequences need
+//     not be cut into segments to fill the GPU; half as many instructions again
+//     per token and channel.  Of four tokens each lane prepares one (step
+//     sizes, gate), and they exchange.
 template <typename T, int LPC>
 struct SpShape {
     static constexpr int kCT = 64;  // channels
@@ -163,7 +181,9 @@ struct SpShape {
     // row pitch: with LPC lanes per channel a warp reads LPC rows at once;
     // 128 / LPC bytes more put them into different banks
     static constexpr int kPitch = kCT + (LPC == 1 ? 0 : 128 / LPC / int(sizeof(T)));
-    static constexpr int kBlocks = LPC == 1 ? 12 : LPC == 2 ? 8 : 4;  // resident per SM
+    // resident per SM: 168 and 128 registers (six blocks of four lanes, 80
+    // registers, spill and were 4 to 20 % slower)
+    static constexpr int kBlocks = LPC == 1 ? 12 : 4;
 };
 
 // What a thread holds of its two channels.

@@ -122,7 +122,9 @@ __device__ __forceinline__ void step_load4(const void *base, int64_t off, int64_
 // A slot past the cache's end, or one that an earlier row of the batch
 // already owns, is refused (the row is skipped and the error word set): two
 // rows on one slot would race on its state.  The block compares the earlier
-// rows' slots itself, 256 per step, from L1.
+// rows' slots itself, 256 per step, from L1, while its state is on the way
+// (256 rows of 5120 x 16 states, bf16: 37.5 us, 40.1 with the look first; 64
+// rows of 32 x 64 x 128: 26.0 and 27.8).
 template <typename T, int TPC, bool SCALAR, bool SLOTS = false>
 __global__ void __launch_bounds__(256, SCALAR ? 8 : 6) step_kernel(StepParams p)
 {
