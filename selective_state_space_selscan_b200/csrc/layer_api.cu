@@ -175,19 +175,23 @@ struct PackedPlan {
 // which does the least work, where the average sequence is cut up in any case
 // (131072 x 2048 in one prompt 1.87 ms, four lanes 2.6; 32768 x 2048, general A,
 // 725 against 757 us); four otherwise (32 prompts: 367 us, one lane 471; 300 x
-// 768 in one: 23 against 43).
+// 768 in one: 23 against 43); eight up to 2^20 elements, where the longest
+// sequence's own time counts (257 x 64 in five 18 us, four lanes 27; 300 x 768
+// in one 19 against 23; but 16000 x 256 in 16 77 against 69).
 PackedPlan packed_plan(int64_t tokens, int64_t seqs, int64_t dim, int64_t sms)
 {
     const int64_t warps1 = (dim + 63) / 64, warps4 = 4 * warps1;
     const auto seg_of = [&](int64_t warps, int64_t slots) {
         return std::max<int64_t>(64, ((tokens * warps + slots - 1) / slots + 15) / 16 * 16);
     };
-    // a few short sequences: one segment each, one launch
-    const int64_t seg4 =
-        tokens <= 512 && tokens <= 64 * seqs ? tokens + 1 : seg_of(warps4, 44 * sms);
+    // short calls in one launch: cut up, they would take three
+    const bool brief = tokens <= 128 || (tokens <= 512 && tokens <= 64 * seqs);
+    const int64_t seg4 = brief ? tokens + 1 : seg_of(warps4, 44 * sms);
     PackedPlan plan;
-    plan.lanes = g_dbg_packed_lanes ? g_dbg_packed_lanes
-                                    : (tokens > 2 * seqs * seg4 && seg4 > 64 ? 1 : 4);
+    plan.lanes = g_dbg_packed_lanes                             ? g_dbg_packed_lanes
+                 : tokens * dim <= (int64_t(1) << 20)           ? 8
+                 : tokens > 2 * seqs * seg4 && seg4 > 64        ? 1
+                                                                : 4;
     const int64_t seg = plan.lanes == 1 ? seg_of(warps1, 16 * sms) : seg4;
     plan.seg_len = g_dbg_packed_seg ? g_dbg_packed_seg : int(std::min(seg, kMaxLen));
     return plan;
@@ -209,6 +213,9 @@ void launch_packed(const ScanPackedParams &p, bool bf, int lanes, unsigned grid,
     if (lanes == 1)
         bf ? launch_packed<__nv_bfloat16, 1, OUT, GATE>(p, grid, s)
            : launch_packed<float, 1, OUT, GATE>(p, grid, s);
+    else if (lanes == 8)
+        bf ? launch_packed<__nv_bfloat16, 8, OUT, GATE>(p, grid, s)
+           : launch_packed<float, 8, OUT, GATE>(p, grid, s);
     else
         bf ? launch_packed<__nv_bfloat16, 4, OUT, GATE>(p, grid, s)
            : launch_packed<float, 4, OUT, GATE>(p, grid, s);
@@ -601,7 +608,7 @@ extern "C" selscan_status selscan_conv_packed(selscan_tensor *state, const selsc
 extern "C" void selscan_debug_packed_segment(int tokens, int lanes)
 {
     g_dbg_packed_seg = tokens <= 0 ? 0 : (tokens + 15) / 16 * 16;
-    g_dbg_packed_lanes = lanes == 1 || lanes == 4 ? lanes : 0;
+    g_dbg_packed_lanes = lanes == 1 || lanes == 4 || lanes == 8 ? lanes : 0;
 }
 
 extern "C" selscan_status selscan_fwd_packed(
@@ -683,7 +690,8 @@ extern "C" selscan_status selscan_fwd_packed(
     p.y_vec = reinterpret_cast<uintptr_t>(y->data) % uintptr_t(2 * es) == 0 &&
               (tokens <= 1 || y->stride[0] % 2 == 0);
     const PackedPlan plan = packed_plan(tokens, p.ix.seqs, dim, di->sm_count);
-    p.tiles = int((dim + 63) / 64);
+    const int64_t ct = plan.lanes == 8 ? 32 : 64;
+    p.tiles = int((dim + ct - 1) / ct);
     p.seg_len = plan.seg_len;
     const int64_t units = tokens / p.seg_len + p.ix.seqs;
     if (units * p.tiles > 0x7fffffffll)

@@ -172,18 +172,23 @@ __device__ __forceinline__ uint64_t gate_pair(uint64_t z)
 //  4: a token takes about a quarter of the time, so that most sequences need
 //     not be cut into segments to fill the GPU; half as many instructions again
 //     per token and channel.  Of four tokens each lane prepares one (step
-//     sizes, gate), and they exchange.
+//     sizes, gate), and they exchange;
+//  8: for the smallest calls, whose time is the longest sequence's, half of
+//     that again: eight tokens at a time, 32 channels (257 tokens of 64 channels
+//     in five prompts, fp32: 18 us, four lanes 27).
 template <typename T, int LPC>
 struct SpShape {
-    static constexpr int kCT = 64;  // channels
+    static constexpr int kCT = LPC == 8 ? 32 : 64;  // channels
     static constexpr int kThreads = kCT / 2 * LPC;
-    static constexpr int kTC = (LPC == 4 ? 64 : 32) / int(sizeof(T));  // tokens staged at once
+    static constexpr int kTC = (LPC == 1 ? 32 : 64) / int(sizeof(T));  // tokens staged at once
     // row pitch: with LPC lanes per channel a warp reads LPC rows at once;
     // 128 / LPC bytes more put them into different banks
     static constexpr int kPitch = kCT + (LPC == 1 ? 0 : 128 / LPC / int(sizeof(T)));
     // resident per SM: 168 and 128 registers (six blocks of four lanes, 80
     // registers, spill and were 4 to 20 % slower)
     static constexpr int kBlocks = LPC == 1 ? 12 : 4;
+    static constexpr int kGroup = LPC == 8 ? 8 : 4;    // tokens worked on together
+    static constexpr int kOwn = kGroup / LPC;          // of these a lane prepares
 };
 
 // What a thread holds of its two channels.
@@ -246,10 +251,10 @@ struct SpPrep {
 };
 
 template <typename T, int LPC, bool SOFT, bool FULL>
-__device__ __forceinline__ SpPrep<4 / LPC> packed_prepare(const SpChannels<LPC> &s, int t0, int n,
+__device__ __forceinline__ SpPrep<SpShape<T, LPC>::kOwn> packed_prepare(const SpChannels<LPC> &s, int t0, int n,
                                                           const T *us, const T *ds)
 {
-    constexpr int P = SpShape<T, LPC>::kPitch, OWN = 4 / LPC;
+    constexpr int P = SpShape<T, LPC>::kPitch, OWN = SpShape<T, LPC>::kOwn;
     SpPrep<OWN> r;
 #pragma unroll
     for (int i = 0; i < OWN; ++i) {
@@ -297,15 +302,15 @@ __device__ __forceinline__ void packed_chunk(SpChannels<LPC> &s, int n, const T 
                                              const T *zs, const float *bc, T *y, int64_t sy)
 {
     constexpr int P = SpShape<T, LPC>::kPitch, TC = SpShape<T, LPC>::kTC, Q = 8 / LPC;
-    constexpr int OWN = 4 / LPC;  // tokens of four that this lane prepares
+    constexpr int G = SpShape<T, LPC>::kGroup, OWN = SpShape<T, LPC>::kOwn;
     SpPrep<OWN> cur = packed_prepare<T, LPC, SOFT, FULL>(s, 0, n, us, ds);
 #pragma unroll 1
-    for (int t0 = 0; t0 < (FULL ? TC : n); t0 += 4) {
+    for (int t0 = 0; t0 < (FULL ? TC : n); t0 += G) {
         const SpPrep<OWN> next =
-            packed_prepare<T, LPC, SOFT, FULL>(s, min(t0 + 4, TC - 4), n, us, ds);
-        uint64_t part[4];
+            packed_prepare<T, LPC, SOFT, FULL>(s, min(t0 + G, TC - G), n, us, ds);
+        uint64_t part[G];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < G; ++i) {
             uint64_t d = cur.dt[i / LPC], x = cur.dx[i / LPC];
             if (LPC > 1) {
                 const int from = (threadIdx.x & (32 - LPC)) + i % LPC;
@@ -318,24 +323,32 @@ __device__ __forceinline__ void packed_chunk(SpChannels<LPC> &s, int n, const T 
             packed_decay<T, LPC, POW>(e[0], s, 0, lo2(d));
             packed_decay<T, LPC, POW>(e[1], s, 1, hi2(d));
             const uint64_t x2[2] = {pk2(lo2(x), lo2(x)), pk2(hi2(x), hi2(x))};
-            const ulonglong2 *row = reinterpret_cast<const ulonglong2 *>(bc + (t0 + i) * 32);
+            const float *row = bc + (t0 + i) * 32;  // B, and C 16 behind it
 #pragma unroll
-            for (int k = 0; k < Q / 2; ++k) {
-                const ulonglong2 B = row[k];
-                const ulonglong2 C = OUT ? row[4 + k] : B;
+            for (int k = 0; k < Q; ++k) {
+                // two pairs at a time where there are two
+                uint64_t B, C;
+                if constexpr (Q > 1) {
+                    const ulonglong2 b2 = reinterpret_cast<const ulonglong2 *>(row)[k / 2];
+                    const ulonglong2 c2 =
+                        OUT ? reinterpret_cast<const ulonglong2 *>(row)[4 + k / 2] : b2;
+                    B = k % 2 ? b2.y : b2.x;
+                    C = k % 2 ? c2.y : c2.x;
+                } else {
+                    B = *reinterpret_cast<const uint64_t *>(row);
+                    C = OUT ? *reinterpret_cast<const uint64_t *>(row + 16) : B;
+                }
 #pragma unroll
                 for (int ch = 0; ch < 2; ++ch) {
-                    uint64_t(&h)[Q] = s.h[ch];
-                    h[2 * k] = fma2(e[ch][2 * k], h[2 * k], mul2(x2[ch], B.x));
-                    h[2 * k + 1] = fma2(e[ch][2 * k + 1], h[2 * k + 1], mul2(x2[ch], B.y));
-                    if (OUT) {
-                        acc[ch][0] = k ? fma2(C.x, h[2 * k], acc[ch][0]) : mul2(C.x, h[0]);
-                        acc[ch][1] = k ? fma2(C.y, h[2 * k + 1], acc[ch][1]) : mul2(C.y, h[1]);
-                    }
+                    uint64_t &h = s.h[ch][k];
+                    h = fma2(e[ch][k], h, mul2(x2[ch], B));
+                    if (OUT)
+                        acc[ch][k % 2] = k > 1 ? fma2(C, h, acc[ch][k % 2]) : mul2(C, h);
                 }
             }
             if (OUT) {
-                const uint64_t a = add2(acc[0][0], acc[0][1]), b = add2(acc[1][0], acc[1][1]);
+                const uint64_t a = Q > 1 ? add2(acc[0][0], acc[0][1]) : acc[0][0];
+                const uint64_t b = Q > 1 ? add2(acc[1][0], acc[1][1]) : acc[1][0];
                 part[i] = add2(pk2(lo2(a), lo2(b)), pk2(hi2(a), hi2(b)));
             }
         }
@@ -351,15 +364,12 @@ __device__ __forceinline__ void packed_chunk(SpChannels<LPC> &s, int n, const T 
             const auto swap = [](uint64_t v, int lanes) {
                 return uint64_t(__shfl_xor_sync(0xffffffffu, (unsigned long long)v, lanes));
             };
-            const bool up = s.j & 2, odd = s.j & 1;
-            if (LPC == 4) {
-                part[0] = add2(up ? part[2] : part[0], swap(up ? part[0] : part[2], 2));
-                part[1] = add2(up ? part[3] : part[1], swap(up ? part[1] : part[3], 2));
-            }
 #pragma unroll
-            for (int i = 0; i < OWN; ++i)
-                part[i] = add2(odd ? part[2 * i + 1] : part[2 * i],
-                               swap(odd ? part[2 * i] : part[2 * i + 1], 1));
+            for (int o = LPC / 2; o > 0; o /= 2)
+#pragma unroll
+                for (int i = 0; i < o; ++i)
+                    part[i] = add2(s.j & o ? part[i + o] : part[i],
+                                   swap(s.j & o ? part[i] : part[i + o], o));
         }
 #pragma unroll
         for (int i = 0; i < OWN; ++i) {
