@@ -75,7 +75,8 @@ SELSCAN_API long long selscan_debug_fwd_plan(long long tiles, long long chunks, 
 /*
  * Tokens per segment of subsequent selscan_fwd_packed calls, rounded up to a
  * multiple of 16 (0, the default: chosen from the numbers of rows, sequences
- * and channels), and lanes per channel (1, 4 or 8; other values: chosen).
+ * and channels), and lanes per channel (1, 4 or 8; -4: four, with the outputs of
+ * first segments in the first pass; other values: chosen).
  */
 SELSCAN_API void selscan_debug_packed_segment(int tokens, int lanes);
 

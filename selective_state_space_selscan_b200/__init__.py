@@ -634,7 +634,8 @@ def debug_bwd_plan(tiles: int, nchunks: int, slots: int) -> int:
 
 def debug_packed_segment(tokens: int, lanes: int = 0) -> None:
     """Test hook: tokens per segment (0: automatic) and lanes per channel (1, 4
-    or 8, 0: automatic) in selscan_fwd_packed."""
+    or 8; -4: four, first segments' outputs in the first pass; 0: automatic) in
+    selscan_fwd_packed."""
     lib().selscan_debug_packed_segment(int(tokens), int(lanes))
 
 

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cstdlib>
 #include <cstdint>
 
 #include "selscan.h"
@@ -164,20 +165,31 @@ int g_dbg_packed_lanes = 0;
 
 struct PackedPlan {
     int lanes;    // per channel
+    bool lead;    // outputs of first segments in the first pass
     int seg_len;  // tokens of a segment
 };
 
 // Lanes per channel and tokens per segment of packed prompts, from the numbers
-// of rows, sequences and channels (the lengths are on the device).  Segments
-// share the rows' work out over a wave or two of warps: 16 per SM with one lane
-// per channel, 44 with four (16384 x 2048 in 32 prompts: 256 tokens 376 us, 512
-// 367, 1024 476; 8192 x 5120 in 64: 256 430, 512 443).  One lane per channel,
-// which does the least work, where the average sequence is cut up in any case
-// (131072 x 2048 in one prompt 1.87 ms, four lanes 2.6; 32768 x 2048, general A,
-// 725 against 757 us); four otherwise (32 prompts: 367 us, one lane 471; 300 x
-// 768 in one: 23 against 43); eight up to 2^20 elements, where the longest
-// sequence's own time counts (257 x 64 in five 18 us, four lanes 27; 300 x 768
-// in one 19 against 23; but 16000 x 256 in 16 77 against 69).
+// of rows, sequences and channels (the lengths are on the device).  All figures
+// bf16 with gate, general A where none is named, us.
+// Lanes: eight up to 2^20 elements, where the longest sequence's own time counts
+// (257 x 64 fp32 in five prompts 18, four lanes 27; 300 x 768 in one 19 against
+// 24; but 16000 x 256 in 16 78 against 70).  One, which does the least work,
+// where the average sequence would be cut up in any case and the rows fill the
+// GPU (131072 x 2048 in one prompt, A[n] = (n+1) A[0], 1840 against 2600; 16384
+// x 2048 in one 377 against 399; but 8192 x 2048 in 16 234 against 197).  Four
+// otherwise (16384 x 2048 in 32 prompts 362, one lane 472).
+// Segments: the rows' share of some waves of warps.  One lane: 16 warps per SM,
+// a wave and a third, and twice, four times, ... as many where segments would be
+// longer than 512, several sequences' than 192, whose ends leave gaps that
+// shorter ones fill (131072 x 2048 1840, unhalved 1872; 32768 x 5120 in two
+// 1720 against 1965; 16384 x 2048 in four 382 against 424).  Four lanes: 44
+// warps per SM; with `lead` 60, since first segments cost no second scan (256
+// tokens 357, 336 364, 512 376).
+// lead: where the rows fill the GPU (32768 x 2048 in 64 prompts 633, without 700;
+// 8192 x 2048 in 16 197 against 205); short of that, the first pass takes as long
+// as its slowest segment, which outputs make slower (16000 x 256 in 16 73 against
+// 70).
 PackedPlan packed_plan(int64_t tokens, int64_t seqs, int64_t dim, int64_t sms)
 {
     const int64_t warps1 = (dim + 63) / 64, warps4 = 4 * warps1;
@@ -187,38 +199,54 @@ PackedPlan packed_plan(int64_t tokens, int64_t seqs, int64_t dim, int64_t sms)
     // short calls in one launch: cut up, they would take three
     const bool brief = tokens <= 128 || (tokens <= 512 && tokens <= 64 * seqs);
     const int64_t seg4 = brief ? tokens + 1 : seg_of(warps4, 44 * sms);
+    const int dbg = g_dbg_packed_lanes;
     PackedPlan plan;
-    plan.lanes = g_dbg_packed_lanes                             ? g_dbg_packed_lanes
-                 : tokens * dim <= (int64_t(1) << 20)           ? 8
-                 : tokens > 2 * seqs * seg4 && seg4 > 64        ? 1
-                                                                : 4;
-    const int64_t seg = plan.lanes == 1 ? seg_of(warps1, 16 * sms) : seg4;
+    plan.lanes = dbg                                       ? std::abs(dbg)
+                 : tokens * dim <= (int64_t(1) << 20)      ? 8
+                 : tokens > 2 * seqs * seg4 && seg4 >= 256 ? 1
+                                                           : 4;
+    plan.lead = dbg ? dbg < 0 : plan.lanes == 4 && !brief && seg4 > 128;
+    int64_t seg = plan.lead ? seg_of(warps4, 60 * sms) : seg4;
+    if (plan.lanes == 1) {
+        int64_t slots = 16 * sms;
+        while ((seg = seg_of(warps1, slots)) > (seqs == 1 ? 512 : 192))
+            slots *= 2;
+    }
     plan.seg_len = g_dbg_packed_seg ? g_dbg_packed_seg : int(std::min(seg, kMaxLen));
     return plan;
 }
 
-template <typename T, int LPC, bool OUT, bool GATE>
-void launch_packed(const ScanPackedParams &p, unsigned grid, cudaStream_t s)
-{
-    constexpr int NT = SpShape<T, LPC>::kThreads;
-    if (p.softplus)
-        scan_packed_kernel<T, LPC, OUT, true, GATE><<<grid, NT, 0, s>>>(p);
-    else
-        scan_packed_kernel<T, LPC, OUT, false, GATE><<<grid, NT, 0, s>>>(p);
-}
-
-template <bool OUT, bool GATE>
+template <bool FIRST, bool GATE, bool SOFT>
 void launch_packed(const ScanPackedParams &p, bool bf, int lanes, unsigned grid, cudaStream_t s)
 {
-    if (lanes == 1)
-        bf ? launch_packed<__nv_bfloat16, 1, OUT, GATE>(p, grid, s)
-           : launch_packed<float, 1, OUT, GATE>(p, grid, s);
-    else if (lanes == 8)
-        bf ? launch_packed<__nv_bfloat16, 8, OUT, GATE>(p, grid, s)
-           : launch_packed<float, 8, OUT, GATE>(p, grid, s);
+    const auto go = [&](auto tag, auto l) {
+        using T = decltype(tag);
+        constexpr int LPC = decltype(l)::value;
+        scan_packed_kernel<T, LPC, FIRST, SOFT, GATE>
+            <<<grid, SpShape<T, LPC>::kThreads, 0, s>>>(p);
+    };
+    const auto with = [&](auto tag) {
+        if constexpr (!(FIRST && GATE)) {
+            if (lanes == 1)
+                return go(tag, std::integral_constant<int, 1>());
+            if (lanes == 8)
+                return go(tag, std::integral_constant<int, 8>());
+        }
+        go(tag, std::integral_constant<int, 4>());
+    };
+    bf ? with(__nv_bfloat16()) : with(float());
+}
+
+template <bool FIRST>
+cudaError_t launch_packed(const ScanPackedParams &p, bool bf, int lanes, unsigned grid, cudaStream_t s)
+{
+    if (p.z && (!FIRST || p.lead))
+        p.softplus ? launch_packed<FIRST, true, true>(p, bf, lanes, grid, s)
+                   : launch_packed<FIRST, true, false>(p, bf, lanes, grid, s);
     else
-        bf ? launch_packed<__nv_bfloat16, 4, OUT, GATE>(p, grid, s)
-           : launch_packed<float, 4, OUT, GATE>(p, grid, s);
+        p.softplus ? launch_packed<FIRST, false, true>(p, bf, lanes, grid, s)
+                   : launch_packed<FIRST, false, false>(p, bf, lanes, grid, s);
+    return counted_launch();
 }
 
 // f(T tag, integral constant W) for the element type and tap count at hand.
@@ -608,7 +636,7 @@ extern "C" selscan_status selscan_conv_packed(selscan_tensor *state, const selsc
 extern "C" void selscan_debug_packed_segment(int tokens, int lanes)
 {
     g_dbg_packed_seg = tokens <= 0 ? 0 : (tokens + 15) / 16 * 16;
-    g_dbg_packed_lanes = lanes == 1 || lanes == 4 || lanes == 8 ? lanes : 0;
+    g_dbg_packed_lanes = lanes == 1 || lanes == 4 || lanes == -4 || lanes == 8 ? lanes : 0;
 }
 
 extern "C" selscan_status selscan_fwd_packed(
@@ -706,19 +734,17 @@ extern "C" selscan_status selscan_fwd_packed(
             return SELSCAN_ERR_CUDA;
         p.agg = static_cast<float *>(ws);
         p.agg_sd = p.agg + entries * size_t(dim) * kDiagN;
-        launch_packed<false, false>(p, bf, plan.lanes, grid, stream);
-        le = counted_launch();
-        if (le == cudaSuccess) {
-            const dim3 fg{unsigned((dim * kDiagN + 255) / 256), unsigned(p.ix.seqs)};
-            scan_packed_fold_kernel<<<fg, 256, 0, stream>>>(p);
-            le = counted_launch();
-        }
     }
-    if (le == cudaSuccess) {
-        gate ? launch_packed<true, true>(p, bf, plan.lanes, grid, stream)
-             : launch_packed<true, false>(p, bf, plan.lanes, grid, stream);
+    p.lead = ws && plan.lead;
+    if (ws)
+        le = launch_packed<true>(p, bf, plan.lanes, grid, stream);
+    if (ws && le == cudaSuccess && tokens > 2 * int64_t(p.seg_len)) {
+        const dim3 fg{unsigned((dim * kDiagN + 255) / 256), unsigned(p.ix.seqs)};
+        scan_packed_fold_kernel<<<fg, 256, 0, stream>>>(p);
         le = counted_launch();
     }
+    if (le == cudaSuccess)
+        le = launch_packed<false>(p, bf, plan.lanes, grid, stream);
     if (ws)
         cudaFreeAsync(ws, stream);
     return le == cudaSuccess ? SELSCAN_OK : SELSCAN_ERR_CUDA;

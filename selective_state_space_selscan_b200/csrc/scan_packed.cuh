@@ -19,7 +19,9 @@
 // The segments of a longer one do not wait for one another: a first pass
 // scans each from zero for its end state E and its sum of step sizes, a small
 // kernel folds these along the sequence (h <- exp(A sum delta) h + E), and
-// the output pass starts each segment from its folded state.
+// the output pass starts each segment from its folded state.  Where there is
+// work enough the first pass also writes the outputs of the first segments
+// (they and the last then cost one scan, and only those between them two).
 //
 // What bounds it.  Not HBM (8 bytes per element and pass): a token of a channel
 // takes 16 decays, 16 inputs, 16 updates and 16 output products.  With a
@@ -29,9 +31,10 @@
 // for about 105 (a packed FMA of three different register pairs issues every
 // third cycle, a packed multiply every second, both measured; scalar FMAs in
 // their place were 2 % (outputs) to 20 % (updates) slower).  Measured, bf16
-// with gate: 131072 x 2048 in one prompt, A[n] = (n+1) A[0], 1.87 ms (pass 1
-// 0.75, output pass 1.15 = 157 cycles); 16384 x 2048 in 32 prompts of
-// log-normal lengths, general A, 0.38 ms; of which 0.13 ms are the first pass.
+// with gate: 131072 x 2048 in one prompt, A[n] = (n+1) A[0], 1.84 ms (pass 1
+// about 0.75, output pass 1.1 = 157 cycles); 16384 x 2048 in 32 prompts of
+// log-normal lengths, general A, 0.36 ms (0.37 where first segments are scanned
+// twice too).
 // Tried and dropped: two of eight pairs of exponentials as polynomials on the
 // FMA pipe (10 to 13 instructions per pair instead of 2: issue-bound, 441
 // against 408 us), two lanes per channel (414 against 393 us), one channel per
@@ -56,6 +59,7 @@ struct ScanPackedParams {
     int dim, seg_len, tiles;
     int vec;            // whole 16-byte pieces of rows may be read
     int y_vec;          // pairs of channels may be written as one word
+    int lead;           // first segments' outputs in the first pass
     int bc_vec;         // whole pieces of four values of B and C may be read
     const void *u, *delta, *z, *B, *C;
     int64_t su, sd, sz, sB, sC;  // row strides
@@ -384,26 +388,30 @@ __device__ __forceinline__ void packed_chunk(SpChannels<LPC> &s, int n, const T 
     }
 }
 
-// OUT false: the first pass of sequences with several segments.
-template <typename T, int LPC, bool OUT, bool SOFT, bool GATE>
+// FIRST: the first pass, for the states at the segments' ends.  With p.lead it
+// also writes the outputs of each sequence's first segment, whose start is
+// known; the second pass then has the others only.
+template <typename T, int LPC, bool FIRST, bool SOFT, bool GATE>
 __global__ void __launch_bounds__(SpShape<T, LPC>::kThreads, SpShape<T, LPC>::kBlocks)
     scan_packed_kernel(const __grid_constant__ ScanPackedParams p)
 {
     using Shape = SpShape<T, LPC>;
     constexpr int TC = Shape::kTC, VEC = 16 / int(sizeof(T));
     constexpr int CT = Shape::kCT, NT = Shape::kThreads, Q = 8 / LPC;
-    constexpr int NS = GATE ? 3 : 2;  // staged rows: u (later y), Delta, z
+    constexpr int NS = GATE ? 3 : 2;  // staged rows: u, Delta, z
+    constexpr bool LEADS = LPC == 4;  // p.lead may be set
     constexpr bool kFast = !std::is_same<T, float>::value;
     __shared__ __align__(16) T tile[2][NS][TC][Shape::kPitch];
     __shared__ __align__(16) float bcf[2][TC][32];
     const PackedIndex &ix = p.ix;
+    const bool lead = LEADS && p.lead, main = FIRST == lead;  // main: runs in any case
     const int tid = threadIdx.x, lane = tid & 31;
     const int ct = int(blockIdx.x % unsigned(p.tiles));
     const int64_t unit = blockIdx.x / unsigned(p.tiles);
 
     // with starts in disorder the search may miss a sequence: the units' first
     // blocks look at all of them
-    if (OUT && ct == 0 && unit < ix.seqs && tid == 0) {
+    if (main && ct == 0 && unit < ix.seqs && tid == 0) {
         const int bg = ix.start[unit], en = ix.start[unit + 1];
         if (ix.slots[unit] >= 0 && (bg < 0 || en < bg || en > ix.tokens))
             atomicOr(ix.err, kErrIndex);
@@ -421,7 +429,7 @@ __global__ void __launch_bounds__(SpShape<T, LPC>::kThreads, SpShape<T, LPC>::kB
     const int n0 = j * (kDiagN / LPC);  // this lane's first state
     float *st = p.state + (int64_t(q.slot) * p.dim + (chans ? c : 0)) * kDiagN + n0;
     if (seg < 0 || lo >= len) {
-        if (OUT && len == 0 && seg == 0 && q.fresh)
+        if (main && len == 0 && seg == 0 && q.fresh)
             for (int ch = 0; ch < chans; ++ch)
                 for (int k = 0; k < kDiagN / LPC; ++k)
                     st[ch * kDiagN + k] = 0.f;
@@ -430,10 +438,16 @@ __global__ void __launch_bounds__(SpShape<T, LPC>::kThreads, SpShape<T, LPC>::kB
     const bool many = len > p.seg_len;
     const int n_all = int(min(int64_t(p.seg_len), len - lo));
     const bool last = lo + n_all >= len;
-    if (!OUT && (!many || last))
+    const bool out = FIRST ? lead && seg == 0 : true;  // y is written
+    if (FIRST ? !out && last : lead && seg == 0)
         return;
-    const int64_t ag = packed_agg(q.begin, p.seg_len) + seg;
-    float *agg = p.agg + (ag * p.dim + (chans ? c : 0)) * kDiagN + n0;
+    const int64_t ag = packed_agg(q.begin, p.seg_len);
+    const int nseg = (len - 1) / p.seg_len + 1;
+    // agg[k] of a sequence: the end of segment k, the start of k + 1; the last
+    // entry the start of the first, where the second pass has that too
+    const auto agg = [&](int64_t k) {
+        return p.agg + ((ag + k) * p.dim + (chans ? c : 0)) * kDiagN + n0;
+    };
 
     const int t_first = q.begin + int(lo);
     const int chunks = (n_all + TC - 1) / TC;
@@ -455,6 +469,8 @@ __global__ void __launch_bounds__(SpShape<T, LPC>::kThreads, SpShape<T, LPC>::kB
         constexpr int STEP = NT / PR;  // rows between a thread's pieces
 #pragma unroll
         for (int v = 0; v < NS; ++v) {
+            if (FIRST && v == 2 && !out)
+                break;
             if (p.vec) {
                 const T *g = at[v];
 #pragma unroll
@@ -486,7 +502,7 @@ __global__ void __launch_bounds__(SpShape<T, LPC>::kThreads, SpShape<T, LPC>::kB
             const int t = k * TC + r;
             const T *m = static_cast<const T *>(o < 16 ? p.B : p.C) +
                          (int64_t(t_first) + t) * (o < 16 ? p.sB : p.sC) + (o & 15);
-            if (r >= TC || t >= n_all || (!OUT && o >= 16)) {
+            if (r >= TC || t >= n_all || (FIRST && !out && o >= 16)) {
                 bcw[l][0] = bcw[l][1] = 0;
             } else if (p.bc_vec) {
                 load_row<T, BV>(m, bcw[l]);
@@ -536,13 +552,22 @@ __global__ void __launch_bounds__(SpShape<T, LPC>::kThreads, SpShape<T, LPC>::kB
                 bias[ch] = p.delta_bias[c + ch];
             if (p.Dskip)
                 dskip[ch] = p.Dskip[c + ch];
-            if (OUT && (many || !q.fresh)) {
-                const float *from = (many ? agg : st) + ch * kDiagN;
+            // the second pass starts from what the first left, the first (and
+            // a sequence of one segment) from the cache
+            const bool left = !FIRST && many;
+            if (left || (seg == 0 && !q.fresh)) {
+                const float *from = (left ? agg(seg ? seg - 1 : nseg - 1) : st) + ch * kDiagN;
 #pragma unroll
                 for (int k = 0; k < Q; ++k) {
                     const float2 v = *reinterpret_cast<const float2 *>(from + 2 * k);
                     s.h[ch][k] = pk2(v.x, v.y);
                 }
+            }
+            if (FIRST && !lead && seg == 0) {
+                float *keep = agg(nseg - 1) + ch * kDiagN;
+#pragma unroll
+                for (int k = 0; k < Q; ++k)
+                    *reinterpret_cast<float2 *>(keep + 2 * k) = make_float2(lo2(s.h[ch][k]), hi2(s.h[ch][k]));
             }
         }
         s.a0 = pk2(a0[0], a0[1]);
@@ -565,45 +590,53 @@ __global__ void __launch_bounds__(SpShape<T, LPC>::kThreads, SpShape<T, LPC>::kB
         const T *us = &tile[buf][0][0][tid / LPC * 2];
         const T *ds = &tile[buf][1][0][tid / LPC * 2], *zs = &tile[buf][NS - 1][0][tid / LPC * 2];
         const float *bc = &bcf[buf][0][n0];
-        T *y = OUT ? static_cast<T *>(p.y) + (t_first + int64_t(k) * TC) * p.sy + c : nullptr;
-        if (kFast && pow && n == TC)
-            packed_chunk<T, LPC, OUT, kFast, SOFT, GATE, kFast>(s, n, us, ds, zs, bc, y, p.sy);
-        else if (n == TC)
-            packed_chunk<T, LPC, OUT, false, SOFT, GATE, true>(s, n, us, ds, zs, bc, y, p.sy);
+        T *y = out ? static_cast<T *>(p.y) + (t_first + int64_t(k) * TC) * p.sy + c : nullptr;
+        const auto scan = [&](auto o) {
+            constexpr bool OUT = decltype(o)::value;
+            if (kFast && pow && n == TC)
+                packed_chunk<T, LPC, OUT, kFast, SOFT, GATE, kFast>(s, n, us, ds, zs, bc, y, p.sy);
+            else if (n == TC)
+                packed_chunk<T, LPC, OUT, false, SOFT, GATE, true>(s, n, us, ds, zs, bc, y, p.sy);
+            else
+                packed_chunk<T, LPC, OUT, false, SOFT, GATE, false>(s, n, us, ds, zs, bc, y, p.sy);
+        };
+        if constexpr (FIRST && LEADS)
+            out ? scan(std::true_type()) : scan(std::false_type());
         else
-            packed_chunk<T, LPC, OUT, false, SOFT, GATE, false>(s, n, us, ds, zs, bc, y, p.sy);
+            scan(std::bool_constant<!FIRST>());
         if (k + 1 < chunks)
             bc_put(k + 1);
     }
-    if (OUT && !last)
+    if (!FIRST && !last)
         return;
     float sum[2] = {lo2(s.sum), hi2(s.sum)};
 #pragma unroll
     for (int ch = 0; ch < 2; ++ch) {
-        if (!OUT)
+        if (FIRST)
 #pragma unroll
             for (int o = 1; o < LPC; o *= 2)
                 sum[ch] += __shfl_xor_sync(0xffffffffu, sum[ch], o);
         if (ch >= chans)
             continue;
-        float *dst = (OUT ? st : agg) + ch * kDiagN;
+        float *dst = (last ? st : agg(seg)) + ch * kDiagN;
 #pragma unroll
         for (int k = 0; k < Q; ++k)
             *reinterpret_cast<float2 *>(dst + 2 * k) = make_float2(lo2(s.h[ch][k]), hi2(s.h[ch][k]));
-        if (!OUT && j == 0)
-            p.agg_sd[ag * p.dim + c + ch] = sum[ch];
+        if (FIRST && !last && j == 0)
+            p.agg_sd[(ag + seg) * p.dim + c + ch] = sum[ch];
     }
 }
 
-// The start state of every segment of the sequences that have several, in
-// place of the segments' end states: one thread per channel and state.
+// The states at the ends of the segments of sequences that have three or more,
+// but for the first's and the last's, in place of what these scanned from zero:
+// one thread per channel and state.
 static __global__ void __launch_bounds__(256) scan_packed_fold_kernel(const __grid_constant__ ScanPackedParams p)
 {
     const PackedIndex &ix = p.ix;
     const int s = int(blockIdx.y);
     const int i = int(blockIdx.x) * 256 + int(threadIdx.x);
     const int begin = ix.start[s], end = ix.start[s + 1];
-    if (int64_t(end) - begin <= p.seg_len)
+    if (int64_t(end) - begin <= 2 * int64_t(p.seg_len))
         return;
     PackedSeq q;
     const PackedView view(ix, threadIdx.x & 31);
@@ -611,16 +644,16 @@ static __global__ void __launch_bounds__(256) scan_packed_fold_kernel(const __gr
         return;
     const int c = i / kDiagN;
     const float a = p.A[i];
-    const int nseg = (end - begin + p.seg_len - 1) / p.seg_len;
+    const int nseg = (end - begin - 1) / p.seg_len + 1;
     const int64_t base = packed_agg(begin, p.seg_len);
     float *ag = p.agg + base * p.dim * kDiagN + i;
     const float *sd = p.agg_sd + base * p.dim + c;
-    float h = q.fresh ? 0.f : p.state[int64_t(q.slot) * p.dim * kDiagN + i];
     const int64_t hop = int64_t(p.dim) * kDiagN;
+    float h = ag[0];
     // eight segments' numbers at a time: one after the other, each would cost a
     // trip to memory (37 segments of 2048 channels: 82 us, now 14)
     constexpr int AHEAD = 8;
-    for (int k0 = 0; k0 < nseg - 1; k0 += AHEAD) {
+    for (int k0 = 1; k0 < nseg - 1; k0 += AHEAD) {
         float E[AHEAD], S[AHEAD];
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
@@ -631,11 +664,10 @@ static __global__ void __launch_bounds__(256) scan_packed_fold_kernel(const __gr
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j)
             if (k0 + j < nseg - 1) {
-                ag[(k0 + j) * hop] = h;
                 h = fmaf(expf(a * S[j]), h, E[j]);
+                ag[(k0 + j) * hop] = h;
             }
     }
-    ag[(nseg - 1) * hop] = h;
 }
 
 }  // namespace selscan

@@ -130,7 +130,7 @@ def test_scan_packed_matches_plain(dtype, D):
                 assert rel(got[rows], y_ref[rows]) <= (1e-5 if dtype == "f32" else 5e-3), (lens, i)
 
 
-@pytest.mark.parametrize("lanes", [1, 4, 8])
+@pytest.mark.parametrize("lanes", [1, 4, -4, 8])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_scan_packed_forms(lanes, dtype):
     """All splits of a channel's states over lanes, in segments of 16 to 48
