@@ -544,8 +544,8 @@ SELSCAN_API int selscan_version(void);
  * copies); selscan_bwd_scalarA launches three (chunk states, the chunk
  * walk, the sum of the dB / dC copies); selscan_conv_bwd launches two (the
  * gradients, the sum of the runs' weight gradients); selscan_fwd_packed one,
- * or three where a sequence may be longer than a segment (segment ends, their
- * fold, the output pass); the other entry points launch one.  Benchmarks read
+ * two where a sequence may have two segments (segment ends, the output pass),
+ * three where it may have more (the fold of the ends between them); the other entry points launch one.  Benchmarks read
  * it around a timed region to report how many of the library's kernels ran in
  * it.
  */

@@ -194,6 +194,36 @@ def test_scan_packed_many_segments():
                 assert rel(host(out)[rows], y_ref[rows]) <= (1e-5 if dtype == "f32" else 5e-3)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D,lens", [
+    (2040, [1500, 100, 2, 900, 0, 430, 700, 1300, 64, 65, 350, 800, 1000, 1, 600, 385]),
+    (1100, [21000, 2, 5800]),
+    (1100, [26000]),
+])
+def test_scan_packed_fills_the_gpu(D, lens, dtype):
+    """Sizes whose automatic split takes first segments' outputs in the first
+    pass, and long prompts with one lane per channel, several and alone; the
+    first and last channels and two in between against fp64."""
+    import selective_state_space_selscan_b200 as ss
+    rng = np.random.default_rng(len(lens))
+    pk = Packed(rng, lens, tail=3, lead=1)
+    inp = scan_inputs(rng, pk.tokens, D, dtype, real=len(lens) == 3)
+    state0, y0 = rnd(rng, pk.count, D, N), rnd(rng, pk.tokens, D, dtype=dtype)
+    ch = np.array([0, 1, 63, 64, D // 2, D - 2, D - 1])
+    part = {k: v if k in "BC" else v[ch] if k in ("A", "D", "delta_bias") else v[:, ch]
+            for k, v in inp.items()}
+    y_ref, s_ref = scan_reference(pk, part, state0[:, ch], y0[:, ch])
+    state, out = dev(state0), dev(y0, dtype)
+    scan_call(pk, inp, state, out, dtype)
+    ss.check()
+    st, y = host(state)[:, ch], host(out)
+    assert np.array_equal(y[~pk.owned], y0[~pk.owned].astype(np.float64))
+    for i, rows, slot in pk.each():
+        assert rel(st[slot], s_ref[slot]) <= 1e-5, i
+        if rows.stop > rows.start:
+            assert rel(y[rows][:, ch], y_ref[rows]) <= (1e-5 if dtype == "f32" else 5e-3), i
+
+
 def test_scan_packed_without_options_and_strided():
     """No bias, D, gate, softplus (negative steps too); operands as column
     slices of wider rows, at odd offsets as well."""
