@@ -80,6 +80,13 @@ SELSCAN_API long long selscan_debug_fwd_plan(long long tiles, long long chunks, 
  */
 SELSCAN_API void selscan_debug_packed_segment(int tokens, int lanes);
 
+/*
+ * Bytes of one load of B or C that selscan_fwd_packed would make on the (tokens,
+ * N) tensor t: a piece of several values (every row's start is a multiple of
+ * that many bytes), or 0, value by value.  Host arithmetic only: no CUDA call.
+ */
+SELSCAN_API long long selscan_debug_packed_piece(const selscan_tensor *t);
+
 #ifdef __cplusplus
 }
 #endif

@@ -133,6 +133,8 @@ def lib() -> ctypes.CDLL:
         L.selscan_debug_bwd_plan.restype = ctypes.c_longlong
         L.selscan_debug_packed_segment.argtypes = [ctypes.c_int] * 2
         L.selscan_debug_packed_segment.restype = None
+        L.selscan_debug_packed_piece.argtypes = [S]
+        L.selscan_debug_packed_piece.restype = ctypes.c_longlong
         _lib = L
     return _lib
 
@@ -637,6 +639,13 @@ def debug_packed_segment(tokens: int, lanes: int = 0) -> None:
     or 8; -4: four, first segments' outputs in the first pass; 0: automatic) in
     selscan_fwd_packed."""
     lib().selscan_debug_packed_segment(int(tokens), int(lanes))
+
+
+def debug_packed_piece(t) -> int:
+    """Test hook: bytes of one load of B or C in selscan_fwd_packed on the
+    (tokens, N) tensor ``t`` (a packed descriptor), 0: value by value.  Host
+    arithmetic only."""
+    return int(lib().selscan_debug_packed_piece(t))
 
 
 def debug_withhold_carry(unit: int) -> None:

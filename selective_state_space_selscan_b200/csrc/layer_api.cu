@@ -312,6 +312,17 @@ bool rows_vec(const selscan_tensor *t, int64_t es)
     return aligned16(t->data) && (t->shape[0] <= 1 || mult16(t->stride[0], es));
 }
 
+// Bytes of one load of B or C of packed prompts: a piece of kPackedBC values (8
+// in bf16, 16 in fp32) where every row's pieces are aligned to that, else 0
+// (value by value).
+int64_t packed_piece_bytes(const selscan_tensor *t)
+{
+    const int64_t es = int64_t(elem_size(t->dtype)), piece = kPackedBC * es;
+    const bool ok = reinterpret_cast<uintptr_t>(t->data) % uintptr_t(piece) == 0 &&
+                    (t->shape[0] <= 1 || (t->stride[0] * es) % piece == 0);
+    return ok ? piece : 0;
+}
+
 }  // namespace
 
 extern "C" selscan_status selscan_conv(const selscan_tensor *x, const selscan_tensor *weight,
@@ -633,6 +644,11 @@ extern "C" selscan_status selscan_conv_packed(selscan_tensor *state, const selsc
     return counted_launch() == cudaSuccess ? SELSCAN_OK : SELSCAN_ERR_CUDA;
 }
 
+extern "C" long long selscan_debug_packed_piece(const selscan_tensor *t)
+{
+    return packed_piece_bytes(t);
+}
+
 extern "C" void selscan_debug_packed_segment(int tokens, int lanes)
 {
     g_dbg_packed_seg = tokens <= 0 ? 0 : (tokens + 15) / 16 * 16;
@@ -691,12 +707,7 @@ extern "C" selscan_status selscan_fwd_packed(
     const int64_t es = int64_t(elem_size(dt));
     p.dim = int(dim);
     p.vec = rows_vec(u, es) && rows_vec(delta, es) && (!gate || rows_vec(z, es));
-    // four bf16 or two fp32 values at a time: 8-byte pieces
-    const auto bc_ok = [&](const selscan_tensor *t) {
-        return reinterpret_cast<uintptr_t>(t->data) % 8 == 0 &&
-               (tokens <= 1 || (t->stride[0] * es) % 8 == 0);
-    };
-    p.bc_vec = bc_ok(B) && bc_ok(C);
+    p.bc_vec = packed_piece_bytes(B) && packed_piece_bytes(C);
     p.u = u->data;
     p.su = u->stride[0];
     p.delta = delta->data;

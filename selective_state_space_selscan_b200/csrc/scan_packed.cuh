@@ -54,13 +54,15 @@
 
 namespace selscan {
 
+constexpr int kPackedBC = 4;  // values of B or C per load, where bc_vec says so
+
 struct ScanPackedParams {
     PackedIndex ix;
     int dim, seg_len, tiles;
     int vec;            // whole 16-byte pieces of rows may be read
     int y_vec;          // pairs of channels may be written as one word
     int lead;           // first segments' outputs in the first pass
-    int bc_vec;         // whole pieces of four values of B and C may be read
+    int bc_vec;         // pieces of kPackedBC values of B and C are aligned loads
     const void *u, *delta, *z, *B, *C;
     int64_t su, sd, sz, sB, sC;  // row strides
     void *y;
@@ -493,7 +495,8 @@ __global__ void __launch_bounds__(SpShape<T, LPC>::kThreads, SpShape<T, LPC>::kB
     };
     // B and C of a chunk: loaded a chunk ahead as they are, widened to fp32
     // when they are stored
-    constexpr int BV = 4, BN = (TC * 32 / BV + NT - 1) / NT;  // values per load, loads
+    constexpr int BV = kPackedBC, BN = (TC * 32 / BV + NT - 1) / NT;  // values per load, loads
+    static_assert(BV == 4, "the pieces below are written out for four values");
     pair_t<T> bcw[BN][BV / 2];
     const auto bc_load = [&](int k) {
 #pragma unroll
