@@ -268,10 +268,9 @@ __device__ __forceinline__ SpPrep<SpShape<T, LPC>::kOwn> packed_prepare(const Sp
         uint64_t d = add2(packed_two(ds + t * P), s.bias);
         if (SOFT)
             d = softplus_pair<T>(d);
-        const uint64_t x = mul2(d, packed_two(us + t * P));
-        // tokens from n on get a zero step, which leaves the state as it is
+        // tokens from n on are not worked on; their step sizes are not summed
+        r.dx[i] = mul2(d, packed_two(us + t * P));
         r.dt[i] = FULL || t < n ? d : 0;
-        r.dx[i] = FULL || t < n ? x : 0;
     }
     return r;
 }
@@ -317,6 +316,12 @@ __device__ __forceinline__ void packed_chunk(SpChannels<LPC> &s, int n, const T 
         uint64_t part[G];
 #pragma unroll
         for (int i = 0; i < G; ++i) {
+            if (!FULL && t0 + i >= n) {
+                // behind the last token (the same for the whole block): nothing
+                // to decay, and exp(0 A) is NaN where A is infinite
+                part[i] = 0;
+                continue;
+            }
             uint64_t d = cur.dt[i / LPC], x = cur.dx[i / LPC];
             if (LPC > 1) {
                 const int from = (threadIdx.x & (32 - LPC)) + i % LPC;
