@@ -85,14 +85,21 @@ __device__ __forceinline__ int64_t packed_agg(int begin, int seg_len)
 // p(f) (a least-maximum fit on |f| <= 1/2, relative error 3e-9 before rounding,
 // whose first coefficient is ln 2, so that factors next to 1, whose products
 // run over thousands of tokens, are not biased), 2^n added to the exponent.
-// x is held to [-125, 127]; `rest` is what x lacks.
-__device__ __forceinline__ uint64_t exp2_pair(uint64_t x, uint64_t rest = 0)
+// x is held to [-125, 128] (2^128 is infinity); `rest` is what x lacks.  The
+// exponent's sum would turn NaN into a number, so a caller whose x may be NaN
+// gets x * 0 in `nan`, to be added to what it makes of the result.
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t x, const uint64_t *rest, uint64_t *nan)
 {
     constexpr float kRound = 12582912.f;  // 1.5 * 2^23: integers in the low bits
     const auto k = [](float v) { return pk2(v, v); };
-    const uint64_t c = pk2(fminf(fmaxf(lo2(x), -125.f), 127.f), fminf(fmaxf(hi2(x), -125.f), 127.f));
+    const auto hold = [](float v) { return min_nan(max_nan(v, -125.f), 128.f); };
+    const uint64_t c = pk2(hold(lo2(x)), hold(hi2(x)));
     const uint64_t t = add2(c, k(kRound));
-    const uint64_t f = add2(add2(c, fma2(t, k(-1.f), k(kRound))), rest);
+    uint64_t f = add2(c, fma2(t, k(-1.f), k(kRound)));
+    if (rest)
+        f = add2(f, *rest);
+    if (nan)
+        *nan = mul2(c, k(0.f));
     uint64_t q = k(0.00015324314881581813f);
     q = fma2(q, f, k(0.0013390958774834871f));
     q = fma2(q, f, k(0.009618517942726612f));
@@ -122,7 +129,8 @@ __device__ __forceinline__ uint64_t exp_pair(uint64_t x)
         x = pk2(fminf(fmaxf(lo2(x), -87.f), 88.f), fminf(fmaxf(hi2(x), -87.f), 88.f));
         const uint64_t m = mul2(x, l);
         const uint64_t lost = fma2(x, l, mul2(m, pk2(-1.f, -1.f)));
-        return exp2_pair(m, fma2(x, pk2(kLog2eLo, kLog2eLo), lost));
+        const uint64_t rest = fma2(x, pk2(kLog2eLo, kLog2eLo), lost);
+        return exp2_pair(m, &rest, nullptr);
     }
 }
 
@@ -209,10 +217,13 @@ struct SpChannels {
 };
 
 // The decays exp(delta A[n]) of one token of channel ch.  POW: A[n] = (n+1)
-// A[0] (bf16), so that they are powers of one exponential.
+// A[0] (bf16), so that they are powers of one exponential.  In fp32 a decay that
+// is NaN comes as a number in e and NaN in nan (else 0), which joins the token's
+// input: beside the exponential's chain instead of at its end (257 x 64 in five
+// prompts 25.1 us, 27.1).
 template <typename T, int LPC, bool POW>
-__device__ __forceinline__ void packed_decay(uint64_t (&e)[8 / LPC], const SpChannels<LPC> &s,
-                                             int ch, float dt)
+__device__ __forceinline__ void packed_decay(uint64_t (&e)[8 / LPC], uint64_t (&nan)[8 / LPC],
+                                             const SpChannels<LPC> &s, int ch, float dt)
 {
     constexpr bool kFast = !std::is_same<T, float>::value;
     constexpr int Q = 8 / LPC;
@@ -235,7 +246,7 @@ __device__ __forceinline__ void packed_decay(uint64_t (&e)[8 / LPC], const SpCha
 #pragma unroll
     for (int k = 0; k < Q; ++k) {
         const uint64_t x = mul2(dt2, s.a2[ch][k]);
-        e[k] = kFast ? pk2(ex2_approx(lo2(x)), ex2_approx(hi2(x))) : exp2_pair(x);
+        e[k] = kFast ? pk2(ex2_approx(lo2(x)), ex2_approx(hi2(x))) : exp2_pair(x, nullptr, &nan[k]);
     }
 }
 
@@ -308,6 +319,7 @@ __device__ __forceinline__ void packed_chunk(SpChannels<LPC> &s, int n, const T 
 {
     constexpr int P = SpShape<T, LPC>::kPitch, TC = SpShape<T, LPC>::kTC, Q = 8 / LPC;
     constexpr int G = SpShape<T, LPC>::kGroup, OWN = SpShape<T, LPC>::kOwn;
+    constexpr bool kFast = !std::is_same<T, float>::value;
     SpPrep<OWN> cur = packed_prepare<T, LPC, SOFT, FULL>(s, 0, n, us, ds);
 #pragma unroll 1
     for (int t0 = 0; t0 < (FULL ? TC : n); t0 += G) {
@@ -330,9 +342,9 @@ __device__ __forceinline__ void packed_chunk(SpChannels<LPC> &s, int n, const T 
             } else if (!OUT) {
                 s.sum = add2(s.sum, d);
             }
-            uint64_t e[2][Q], acc[2][2];
-            packed_decay<T, LPC, POW>(e[0], s, 0, lo2(d));
-            packed_decay<T, LPC, POW>(e[1], s, 1, hi2(d));
+            uint64_t e[2][Q], nan[2][Q], acc[2][2];
+            packed_decay<T, LPC, POW>(e[0], nan[0], s, 0, lo2(d));
+            packed_decay<T, LPC, POW>(e[1], nan[1], s, 1, hi2(d));
             const uint64_t x2[2] = {pk2(lo2(x), lo2(x)), pk2(hi2(x), hi2(x))};
             const float *row = bc + (t0 + i) * 32;  // B, and C 16 behind it
 #pragma unroll
@@ -352,7 +364,8 @@ __device__ __forceinline__ void packed_chunk(SpChannels<LPC> &s, int n, const T 
 #pragma unroll
                 for (int ch = 0; ch < 2; ++ch) {
                     uint64_t &h = s.h[ch][k];
-                    h = fma2(e[ch][k], h, mul2(x2[ch], B));
+                    const uint64_t in = kFast ? mul2(x2[ch], B) : fma2(x2[ch], B, nan[ch][k]);
+                    h = fma2(e[ch][k], h, in);
                     if (OUT)
                         acc[ch][k % 2] = k > 1 ? fma2(C, h, acc[ch][k % 2]) : mul2(C, h);
                 }

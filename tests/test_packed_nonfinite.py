@@ -50,3 +50,86 @@ def test_infinite_decay_rates_reset_the_state(dtype, real):
             same(host(out), y_ref, 1e-5 if dtype == "f32" else 5e-3, form)
     finally:
         ss.debug_packed_segment(0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("where", ["u", "delta", "z", "B", "C", "A", "D", "delta_bias", "state"])
+def test_nan_reaches_what_it_should(where, dtype):
+    """One NaN in an operand, in sequences of one and more segments: the outputs
+    and states that the fp64 form makes NaN, and no others."""
+    rng = np.random.default_rng(61)
+    D = 40
+    pk = Packed(rng, [5, 30, 100, 1], tail=3)
+    pk.seen[:] = 7
+    inp = scan_inputs(rng, pk.tokens, D, dtype)
+    state0, y0 = rnd(rng, pk.count, D, N), rnd(rng, pk.tokens, D, dtype=dtype)
+    for at in (0, 17, 96):  # a token in the first, an inner and the last segment
+        bad, st = {k: v.copy() for k, v in inp.items()}, state0.copy()
+        for i in (1, 2):
+            t = int(pk.start[i]) + min(at, pk.lens[i] - 1)
+            if where in ("u", "delta", "z"):
+                bad[where][t, 21 + i] = np.nan
+            elif where in ("B", "C"):
+                bad[where][t, 9 + i] = np.nan
+            elif where == "A":
+                bad[where][21 + i, at % N] = np.nan
+            elif where == "state":
+                st[pk.slots[i], 21 + i, at % N] = np.nan
+            else:
+                bad[where][21 + i] = np.nan
+        y_ref, s_ref = scan_reference(pk, bad, st, y0)
+        assert np.isnan(y_ref).any()
+        try:
+            for form in FORMS:
+                ss.debug_packed_segment(*form)
+                state, out = dev(st), dev(y0, dtype)
+                scan_call(pk, bad, state, out, dtype)
+                ss.check()
+                same(host(state), s_ref, 1e-5, (where, at, form))
+                same(host(out), y_ref, 1e-5 if dtype == "f32" else 5e-3, (where, at, form))
+        finally:
+            ss.debug_packed_segment(0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_decays_up_to_the_largest_number(dtype):
+    """Positive A: exp(delta A) up to 2^128 is a number, from there infinity.
+
+    One step takes a state of 1e-30 to exp(x) of it, and zero steps keep it.  The
+    exponent x = 2 A goes through A log2 e (constant and product) and the product
+    with the step, 1.3e-8 + 2 x 2^-24 = 1.4e-7 of it at most, so exp(x) is off by
+    1.4e-7 x of itself, and by 2^-20 for the exponential and the products."""
+    rng = np.random.default_rng(62)
+    x = np.array([60.0, 87.0, 87.9, 88.3, 88.6, 88.7, 88.8, 89.0, 95.0, 120.0, 1e4, np.inf])
+    D = len(x)
+    pk = Packed(rng, [1, 20, 60])
+    pk.seen[:] = 1
+    zero = np.zeros((pk.tokens, D), np.float32)
+    inp = dict(u=zero, delta=zero.copy(), B=rnd(rng, pk.tokens, N, dtype=dtype),
+               C=rnd(rng, pk.tokens, N, dtype=dtype), z=zero, D=np.zeros(D, np.float32),
+               A=np.repeat((x / 2).astype(np.float32)[:, None], N, 1),
+               delta_bias=np.zeros(D, np.float32))
+    inp["delta"][pk.start[:-1]] = 2.0
+    state0 = (1e-30 * (1 + np.abs(rng.standard_normal((pk.count, D, N))))).astype(np.float32)
+    e = np.float64(2) * inp["A"][:, 0]
+    big = e >= 128 * np.log(2)
+    assert big.sum() == 6 and not (np.abs(e - 128 * np.log(2)) < 1e-2).any()
+    finite = np.isfinite(e)  # exp(0 A) is NaN where A is infinite
+    try:
+        for form in FORMS:
+            ss.debug_packed_segment(*form)
+            state = dev(state0)
+            scan_call(pk, inp, state, None, dtype, gate=False, delta_softplus=False)
+            ss.check()
+            got = host(state)
+            for i, rows, slot in pk.each():
+                if pk.lens[i] > 1:
+                    assert np.isnan(got[slot][~finite]).all(), (form, i)
+                else:
+                    assert np.isinf(got[slot][~finite]).all(), (form, i)
+                assert np.isposinf(got[slot][big & finite]).all(), (form, i)
+                want = state0[slot].astype(np.float64)[~big] * np.exp(e[~big])[:, None]
+                off = np.abs(got[slot][~big] / want - 1)
+                assert (off <= (1.4e-7 * e[~big] + 2.0 ** -20)[:, None]).all(), (form, i, off.max())
+    finally:
+        ss.debug_packed_segment(0)
