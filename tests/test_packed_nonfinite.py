@@ -133,3 +133,33 @@ def test_decays_up_to_the_largest_number(dtype):
                 assert (off <= (1.4e-7 * e[~big] + 2.0 ** -20)[:, None]).all(), (form, i, off.max())
     finally:
         ss.debug_packed_segment(0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_growing_decays_leave_an_empty_state_empty(dtype):
+    """A = +1 and a sum of steps of about 96 per segment of 48 tokens, whose
+    exponential is infinite: the state of a fresh sequence is zero until its first
+    input, in the last segment, and a number from there."""
+    rng = np.random.default_rng(63)
+    D = 40
+    pk = Packed(rng, [200, 3, 240])
+    pk.seen[:] = 0
+    inp = scan_inputs(rng, pk.tokens, D, dtype)
+    inp["A"][::2, ::3] = 1.0
+    inp["delta"][:] = 2.0
+    inp["delta_bias"][:] = 0.0
+    for i in (0, 2):
+        inp["u"][pk.start[i]:pk.start[i + 1] - 6] = 0
+    state0, y0 = rnd(rng, pk.count, D, N), rnd(rng, pk.tokens, D, dtype=dtype)
+    y_ref, s_ref = scan_reference(pk, inp, state0, y0, softplus=False)
+    assert np.isfinite(s_ref).all()
+    try:
+        for lanes in (1, 4, -4, 8):
+            ss.debug_packed_segment(48, lanes)
+            state, out = dev(state0), dev(y0, dtype)
+            scan_call(pk, inp, state, out, dtype, delta_softplus=False)
+            ss.check()
+            same(host(state), s_ref, 1e-5, lanes)
+            same(host(out), y_ref, 1e-5 if dtype == "f32" else 5e-3, lanes)
+    finally:
+        ss.debug_packed_segment(0)
