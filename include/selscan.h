@@ -333,8 +333,9 @@ SELSCAN_API selscan_status selscan_step_scalarA_slots(
  * left as they were, as are rows that belong to no sequence.  A sequence
  * whose rows leave the buffer, whose slot is past the cache's end, or whose
  * slot an earlier sequence has, is refused on the device: it is skipped and
- * selscan_check() returns SELSCAN_ERR_INDEX.  (With starts that are not
- * non-decreasing, rows may be written more than once or not at all.)
+ * selscan_check() returns SELSCAN_ERR_INDEX.  With starts that go back, those of
+ * padding sequences among them, rows may be written more than once or not at
+ * all; selscan_check() then returns SELSCAN_ERR_INDEX too.
  *
  * N must be 16; at most 65535 sequences.  Arithmetic as in selscan_fwd.
  * Sequences longer than a segment (a length chosen from the number of rows

@@ -798,6 +798,14 @@ struct PackedIndex {
     const int *slots;  // (seqs)
     const int *seen;   // (seqs) or null: tokens already in the state, 0 = start from zero
     unsigned int *err;
+
+    // Whether sequence s (rows [bg, en)) is to be reported: its rows are not in
+    // the buffer, or, be it padding or not, the next sequence begins before it:
+    // the search for a row's sequence may then miss others.
+    __device__ __forceinline__ bool disorder(int s, int bg, int en, bool owns) const
+    {
+        return (owns && (bg < 0 || en < bg || en > tokens)) || (s + 1 < seqs && en < bg);
+    }
 };
 
 struct PackedSeq {
@@ -1073,7 +1081,7 @@ __global__ void __launch_bounds__(128, 3) conv_packed_kernel(const __grid_consta
             if (s < ix.seqs) {
                 const int bg = ix.start[s], en = ix.start[s + 1];
                 const bool owns = ix.slots[s] >= 0;
-                if (owns && (bg < 0 || en < bg || en > ix.tokens))
+                if (ix.disorder(s, bg, en, owns))
                     atomicOr(ix.err, kErrIndex);
                 empty = owns && bg == en && ix.seen && ix.seen[s] <= 0;
             }

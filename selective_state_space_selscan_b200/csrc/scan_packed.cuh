@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(SpShape<T, LPC>::kThreads, SpShape<T, LPC>::kB
     // blocks look at all of them
     if (main && ct == 0 && unit < ix.seqs && tid == 0) {
         const int bg = ix.start[unit], en = ix.start[unit + 1];
-        if (ix.slots[unit] >= 0 && (bg < 0 || en < bg || en > ix.tokens))
+        if (ix.disorder(int(unit), bg, en, ix.slots[unit] >= 0))
             atomicOr(ix.err, kErrIndex);
     }
     const PackedView view(ix, lane);
