@@ -1370,9 +1370,14 @@ __global__ void __launch_bounds__(128, 5) conv_bwd_kernel(const __grid_constant_
                     g[i] = PairOf<T>::f2(yq[i]);
                     if (decltype(silu)::value)
                         g[i] = silu_grad2<T>(tap_sum<W>(w, e, bias), g[i]);
+                    // Behind the end g is zero, but e still holds the last
+                    // inputs: zero times an infinite one is no part of the sum.
+                    // (With SiLU such an input makes the g of its own tokens
+                    // NaN, and with it every tap's sum.)
+                    if (decltype(silu)::value || t0 + i < p.L)
 #pragma unroll
-                    for (int k = 0; k < W; ++k)
-                        dw[q][k] = fma2(g[i], e[k], dw[q][k]);
+                        for (int k = 0; k < W; ++k)
+                            dw[q][k] = fma2(g[i], e[k], dw[q][k]);
                     db[q] = add2(db[q], g[i]);
                 }
             });
