@@ -21,6 +21,7 @@ import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libselscan.so")
+BIND_PATH = os.path.join(_PKG, "_bind.so")
 
 SELSCAN_F32 = 0
 SELSCAN_BF16 = 1
@@ -236,17 +237,45 @@ _bound = None      # its call(entry, stream handle or None, arguments...)
 _bound_empty = None  # its empty(like, fp32, sizes...)
 
 
+def bind_stamp() -> str:
+    """What _bind.so depends on beside its source: the torch and the Python whose
+    object layouts it reads.  Built into the file."""
+    import sys
+
+    import torch
+    return (f"selscan _bind.so for torch {torch.__version__}, "
+            f"Python {sys.version_info[0]}.{sys.version_info[1]};")
+
+
+def bind_fits(path: str = BIND_PATH) -> bool:
+    """Whether the file at ``path`` was built for this torch and Python."""
+    try:
+        with open(path, "rb") as f:
+            return bind_stamp().encode() in f.read()
+    except OSError:
+        return False
+
+
 def _binding():
-    """_bind.so's call, or False where it is not built for this torch."""
+    """_bind.so's call, or False where it is not built for this torch (a file
+    built for another one is not loaded: it would read other layouts)."""
     global _bound, _bound_empty
     if _bound is None:
         import torch  # noqa: F401  (its libraries come first)
         lib()
-        try:
-            from . import _bind
-            _bound, _bound_empty = _bind.call, _bind.empty
-        except ImportError:
-            _bound = False
+        _bound = False
+        if bind_fits():
+            try:
+                from . import _bind
+                _bound, _bound_empty = _bind.call, _bind.empty
+            except ImportError:
+                pass
+        elif os.path.exists(BIND_PATH):
+            import warnings
+            warnings.warn(f"{BIND_PATH} was built for another torch or Python: small calls go "
+                          "through ctypes until it is built again "
+                          "(`python -m selective_state_space_selscan_b200.build`)",
+                          RuntimeWarning, stacklevel=3)
     return _bound
 
 

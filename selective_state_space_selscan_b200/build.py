@@ -9,12 +9,14 @@ import os
 import subprocess
 import sys
 
+from . import BIND_PATH as BIND
+from . import bind_fits, bind_stamp
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libselscan.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("selscan_api.cu", "layer_api.cu")]
-BIND = os.path.join(PKG, "_bind.so")
 BIND_SRC = os.path.join(CSRC, "bind.cpp")
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC)
                   if f.endswith((".cuh", ".h"))] + [
@@ -64,9 +66,9 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
 
 def build_bind(force: bool = False, verbose: bool = False) -> str:
     """Compile _bind.so (tensors to the C ABI, csrc/bind.cpp) against the
-    installed torch, unless it is newer than its sources."""
+    installed torch, unless it was built for that and is newer than its sources."""
     header = os.path.join(ROOT, "include", "selscan.h")
-    if (not force and os.path.exists(BIND)
+    if (not force and bind_fits(BIND)
             and os.path.getmtime(BIND) >= max(os.path.getmtime(p) for p in (BIND_SRC, header))):
         return BIND
     import sysconfig
@@ -79,7 +81,8 @@ def build_bind(force: bool = False, verbose: bool = False) -> str:
            os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")]
     tmp = BIND + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
-           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-fvisibility=hidden", f'-DSELSCAN_BIND_STAMP="{bind_stamp()}"',
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[f"-I{p}" for p in inc], "-o", tmp, BIND_SRC, "-L", PKG, "-l:libselscan.so",
            "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
            "-Wl,-rpath,$ORIGIN"]

@@ -11,6 +11,14 @@
 
 #include "selscan.h"
 
+// The torch and the Python that this file is built for (build.py): the package
+// looks for it in the file before it loads it.
+#ifndef SELSCAN_BIND_STAMP
+#error "define SELSCAN_BIND_STAMP"
+#endif
+extern "C" __attribute__((used, visibility("default"))) const char selscan_bind_stamp[] =
+    SELSCAN_BIND_STAMP;
+
 namespace {
 
 struct Args {
