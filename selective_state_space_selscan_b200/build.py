@@ -64,20 +64,40 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     return LIB
 
 
-def build_bind(force: bool = False, verbose: bool = False) -> str:
+def bind_headers() -> list[str]:
+    """Directories of the headers that csrc/bind.cpp needs, or none where torch's
+    or Python's are not installed."""
+    import importlib.util
+    import sysconfig
+
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return []
+    base = os.path.join(spec.submodule_search_locations[0], "include")
+    dirs = [base, os.path.join(base, "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"]]
+    wanted = (os.path.join(base, "torch", "csrc", "autograd", "python_variable.h"),
+              os.path.join(dirs[2], "Python.h"))
+    return dirs if all(os.path.exists(p) for p in wanted) else []
+
+
+def build_bind(force: bool = False, verbose: bool = False) -> str | None:
     """Compile _bind.so (tensors to the C ABI, csrc/bind.cpp) against the
-    installed torch, unless it was built for that and is newer than its sources."""
+    installed torch, unless it was built for that and is newer than its sources.
+    None, with a note, where torch's or Python's headers are not installed: every
+    call then goes through ctypes, which needs none."""
+    dirs = bind_headers()
+    if not dirs:
+        print("no headers of torch or Python here: _bind.so is not built, calls go through ctypes",
+              file=sys.stderr)
+        return None
     header = os.path.join(ROOT, "include", "selscan.h")
     if (not force and bind_fits(BIND)
             and os.path.getmtime(BIND) >= max(os.path.getmtime(p) for p in (BIND_SRC, header))):
         return BIND
-    import sysconfig
-
     import torch
     base = os.path.dirname(torch.__file__)
-    inc = [os.path.join(ROOT, "include"), os.path.join(base, "include"),
-           os.path.join(base, "include", "torch", "csrc", "api", "include"),
-           sysconfig.get_paths()["include"],
+    inc = [os.path.join(ROOT, "include"), *dirs,
            os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")]
     tmp = BIND + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",

@@ -56,3 +56,15 @@ def test_a_file_for_another_torch_is_built_again(monkeypatch):
     except subprocess.CalledProcessError:
         pass
     assert len(ran) == 1 and any(ss.bind_stamp() in a for a in ran[0])
+
+
+def test_build_without_headers_leaves_the_binding_out(monkeypatch, capsys):
+    """The library itself needs no headers of torch's: the build goes on."""
+    assert all(os.path.isdir(d) for d in build.bind_headers()) and build.bind_headers()
+    real = os.path.exists
+    for missing in ("python_variable.h", "Python.h"):
+        monkeypatch.setattr(build.os.path, "exists",
+                            lambda p, m=missing: not str(p).endswith(m) and real(p))
+        assert build.bind_headers() == []
+        assert build.build_bind(force=True) is None
+        assert "ctypes" in capsys.readouterr().err
