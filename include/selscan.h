@@ -523,7 +523,8 @@ SELSCAN_API selscan_status selscan_bwd_scalarA(
 
 /*
  * selscan_check -- synchronise `stream` and report device-side errors that
- * earlier calls recorded (a bounded wait that gave up returns
+ * earlier calls recorded on the current device, which must be the stream's (a
+ * bounded wait that gave up returns
  * SELSCAN_ERR_TIMEOUT, otherwise a refused slot or sequence returns
  * SELSCAN_ERR_INDEX; the record is then cleared).  Returns
  * SELSCAN_ERR_CUDA if the synchronisation itself failed.

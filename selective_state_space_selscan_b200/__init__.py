@@ -627,9 +627,16 @@ def selscan_conv_packed(state, x, weight, start, slots, bias=None, silu=True, se
 
 
 def check(stream=None) -> None:
-    """Synchronise ``stream`` and raise if a device-side wait timed out or a
-    slot or sequence was refused on the device."""
-    rc = lib().selscan_check(_stream_handle(stream))
+    """Synchronise ``stream`` (by default the current device's current one) and
+    raise if a device-side wait timed out or a slot or sequence was refused on
+    its device.  Each device keeps a record of its own: for calls on tensors of
+    another device than the current one, pass a stream of that device."""
+    if stream is None:
+        rc = lib().selscan_check(_stream_handle(None))
+    else:
+        import torch
+        with torch.cuda.device(stream.device):
+            rc = lib().selscan_check(_stream_handle(stream))
     if rc != 0:
         raise SelscanError(rc, "selscan_check")
 
