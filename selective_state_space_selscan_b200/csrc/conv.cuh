@@ -1215,14 +1215,6 @@ struct ConvBwdParams {
     int silu;
 };
 
-// A warp walks a run of token tiles from the last to the first.  Per tile a
-// thread recomputes v of its CH channels x TB tokens, forms g, adds g e to
-// the taps' gradients, and forms dx, for which it needs the first W-1 g of
-// the tokens behind its own: those of the lane that holds the next token
-// block (a shuffle), or, for the warp's last block, of the first block of the
-// tile done before.  Those behind the run are recomputed first.  The next
-// tile's vectors are on their way into shared memory, each lane's into places
-// of its own, while a tile is computed.
 // A lane's pieces of a tile that is not all inside whole vectors: an end of the
 // sequence, odd channels, unaligned rows (zeros behind the end).
 template <typename T, bool TOK, int CH, int TB, int HLO>
@@ -1239,14 +1231,24 @@ __device__ __forceinline__ void stage_edge(typename BlockIO<T, TOK, CH, TB, HLO>
 // channels: 168 and 12 warps, 87 us instead of 79 for 8 x 2560 x 2048 bf16).
 constexpr int kConvBwdCh = 2;
 
+// A warp walks a run of token tiles from the last to the first.  Per tile a
+// thread recomputes v of its CH channels x TB tokens, forms g, adds g e to
+// the taps' gradients, and forms dx, for which it needs the first W-1 g of
+// the tokens behind its own: those of the lane that holds the next token
+// block (a shuffle), or, for the warp's last block, of the first block of the
+// tile done before.  Those behind the run are recomputed first.  The next
+// tile's vectors are on their way into shared memory, each lane's into places
+// of its own, while a tile is computed.
 template <typename T, int W, bool XTOK, bool YTOK>
 __global__ void __launch_bounds__(128, 5) conv_bwd_kernel(const __grid_constant__ ConvBwdParams p)
 {
     constexpr int CH = kConvBwdCh, TB = 16 / int(sizeof(T)), Q = CH / 2, H = W - 1;
     using XIO = BlockIO<T, XTOK, CH, TB, H>;
     using YIO = BlockIO<T, YTOK, CH, TB, 0>;
-    // tiles staged: the next one too where 48 KB hold it beside the taps
-    constexpr int NS = (XIO::N * XIO::BYTES + YIO::N * YIO::BYTES) * 32 * 8 <= 46000 ? 2 : 1;
+    constexpr int NS = 2;  // tiles staged: this one and the next
+    static_assert((XIO::N * XIO::BYTES + YIO::N * YIO::BYTES) * 32 * 4 * NS +
+                          int(sizeof(ConvTaps<W, 64 * CH>)) <= 48 * 1024,
+                  "both tiles of four warps beside the taps in static shared memory");
     __shared__ __align__(16) ConvTaps<W, 64 * CH> taps;
     __shared__ typename XIO::Piece xring[4][NS][XIO::N][32];
     __shared__ typename YIO::Piece yring[4][NS][YIO::N][32];
@@ -1306,13 +1308,11 @@ __global__ void __launch_bounds__(128, 5) conv_bwd_kernel(const __grid_constant_
     if (above && tg == 0)
         fetch(p.steps);  // the block behind the run
     cp_async_commit();
-    if (NS > 1) {
-        fetch(p.steps - 1);
-        cp_async_commit();
-    }
+    fetch(p.steps - 1);
+    cp_async_commit();
     if (above) {
         // the first W-1 g behind the run
-        cp_async_wait<NS - 1>();
+        cp_async_wait<1>();
         if (tg == 0) {
             const typename XIO::Piece *xr = &xring[wp][p.steps % NS][0][lane];
             const typename YIO::Piece *yr = &yring[wp][p.steps % NS][0][lane];
@@ -1337,10 +1337,10 @@ __global__ void __launch_bounds__(128, 5) conv_bwd_kernel(const __grid_constant_
         }
     }
     for (int step = p.steps - 1; step >= 0; --step) {
-        fetch(NS > 1 ? step - 1 : step);
+        fetch(step - 1);
         cp_async_commit();
         const int64_t tl = first + int64_t(step) * tile;  // the tile's first token
-        cp_async_wait<NS - 1>();
+        cp_async_wait<1>();
         if (tl >= p.L)
             continue;  // nothing there: g is zero (uniform over the warp)
         const int t0 = start(step);

@@ -220,7 +220,7 @@ __device__ __forceinline__ void cp_async16(void *smem_dst, const void *gsrc, uin
                  :: "r"(smem_addr(smem_dst)), "l"(gsrc), "r"(src_bytes) : "memory");
 }
 
-// 8 or 16 bytes by way of the L1 (neighbouring threads read them again).
+// 4, 8 or 16 bytes by way of the L1 (neighbouring threads read them again).
 template <int BYTES>
 __device__ __forceinline__ void cp_async_ca(void *smem_dst, const void *gsrc)
 {

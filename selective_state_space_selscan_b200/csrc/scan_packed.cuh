@@ -134,7 +134,9 @@ __device__ __forceinline__ uint64_t exp_pair(uint64_t x)
     }
 }
 
-// 1 / d of a pair, d in [1, 2^127]: in fp32 with a Newton step.
+// 1 / d of a pair, d >= 1: in fp32 with a Newton step.  Above 2^126 the result
+// is 0 (the unit flushes what is below the normal numbers); a gate is then 0
+// where z sigmoid(z) is below 1.1e-36.
 template <typename T>
 __device__ __forceinline__ uint64_t recip_pair(uint64_t d)
 {
