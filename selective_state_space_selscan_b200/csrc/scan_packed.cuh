@@ -85,14 +85,15 @@ __device__ __forceinline__ int64_t packed_agg(int begin, int seg_len)
 // p(f) (a least-maximum fit on |f| <= 1/2, relative error 3e-9 before rounding,
 // whose first coefficient is ln 2, so that factors next to 1, whose products
 // run over thousands of tokens, are not biased), 2^n added to the exponent.
-// x is held to [-125, 128] (2^128 is infinity); `rest` is what x lacks.  The
-// exponent's sum would turn NaN into a number, so a caller whose x may be NaN
-// gets x * 0 in `nan`, to be added to what it makes of the result.
+// x is held to [-127, 128], whose ends come out as 0 and infinity (between 2^-127
+// and 2^-126 the exponent's sum is off by less than 2^-126); `rest` is what x
+// lacks.  The exponent's sum would turn NaN into a number, so a caller whose x may
+// be NaN gets x * 0 in `nan`, to be added to what it makes of the result.
 __device__ __forceinline__ uint64_t exp2_pair(uint64_t x, const uint64_t *rest, uint64_t *nan)
 {
     constexpr float kRound = 12582912.f;  // 1.5 * 2^23: integers in the low bits
     const auto k = [](float v) { return pk2(v, v); };
-    const auto hold = [](float v) { return min_nan(max_nan(v, -125.f), 128.f); };
+    const auto hold = [](float v) { return min_nan(max_nan(v, -127.f), 128.f); };
     const uint64_t c = pk2(hold(lo2(x)), hold(hi2(x)));
     const uint64_t t = add2(c, k(kRound));
     uint64_t f = add2(c, fma2(t, k(-1.f), k(kRound)));

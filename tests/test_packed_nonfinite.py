@@ -163,3 +163,35 @@ def test_growing_decays_leave_an_empty_state_empty(dtype):
             same(host(out), y_ref, 1e-5 if dtype == "f32" else 5e-3, lanes)
     finally:
         ss.debug_packed_segment(0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_large_steps_forget_large_states(dtype):
+    """A step of delta |A| >= 100 leaves nothing of a state of 1e36 (exp(-100) of
+    it is 4e-8, and from 104 on the decay is zero in fp32): the state is the step's
+    own input, whichever form the call takes."""
+    rng = np.random.default_rng(64)
+    D = 40
+    pk = Packed(rng, [1, 60, 33])
+    pk.seen[:] = 1
+    inp = scan_inputs(rng, pk.tokens, D, dtype)
+    inp["A"] = np.repeat(np.linspace(-110, -4000, D, dtype=np.float32)[:, None], N, 1)
+    inp["delta"][:], inp["delta_bias"][:] = 1.0, 0.0
+    inp["B"] = np.where(np.abs(inp["B"]) < 0.25, np.float32(0.5), inp["B"])
+    inp["u"] = np.where(np.abs(inp["u"]) < 0.25, np.float32(0.5), inp["u"])
+    state0 = (1e36 * (1 + rng.random((pk.count, D, N)))).astype(np.float32)
+    try:
+        for form in FORMS:
+            ss.debug_packed_segment(*form)
+            state = dev(state0)
+            scan_call(pk, inp, state, None, dtype, delta_softplus=False)
+            ss.check()
+            for i, rows, slot in pk.each():
+                t = rows.stop - 1
+                want = inp["u"][t].astype(np.float64)[:, None] * inp["B"][t].astype(np.float64)
+                off = np.abs(host(state)[slot] - want)
+                # what is left of the state after the one step of the first sequence
+                kept = np.abs(state0[slot].astype(np.float64)) * np.exp(inp["A"].astype(np.float64))
+                assert (off <= 2.0 ** -22 * np.abs(want) + kept).all(), (form, i, off.max())
+    finally:
+        ss.debug_packed_segment(0)
