@@ -337,7 +337,11 @@ SELSCAN_API selscan_status selscan_step_scalarA_slots(
  * padding sequences among them, rows may be written more than once or not at
  * all; selscan_check() then returns SELSCAN_ERR_INDEX too.
  *
- * N must be 16; at most 65535 sequences.  Arithmetic as in selscan_fwd.
+ * N must be 16; at most 65535 sequences (batches of many single tokens are
+ * faster through selscan_step_slots).  Arithmetic is fp32, with exponentials
+ * of the library's own: with F32 tensors a decay exp(delta A) of 2^-126 and more
+ * is off by at most 2^-23 + 1.4e-7 |delta A| of itself; below 2^-127 it is 0, from
+ * 2^128 on infinity.
  * Sequences longer than a segment (a length chosen from the number of rows
  * and channels) are scanned in two passes, with the segments' end states in
  * stream-ordered scratch.
@@ -524,9 +528,8 @@ SELSCAN_API selscan_status selscan_bwd_scalarA(
 /*
  * selscan_check -- synchronise `stream` and report device-side errors that
  * earlier calls recorded on the current device, which must be the stream's (a
- * bounded wait that gave up returns
- * SELSCAN_ERR_TIMEOUT, otherwise a refused slot or sequence returns
- * SELSCAN_ERR_INDEX; the record is then cleared).  Returns
+ * bounded wait that gave up returns SELSCAN_ERR_TIMEOUT, otherwise a refused slot
+ * or sequence returns SELSCAN_ERR_INDEX; the record is then cleared).  Returns
  * SELSCAN_ERR_CUDA if the synchronisation itself failed.
  */
 SELSCAN_API selscan_status selscan_check(cudaStream_t stream);

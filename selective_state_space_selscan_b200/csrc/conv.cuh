@@ -20,10 +20,12 @@
 // What bounds them is HBM in the end (4 bytes per element forward, 6 backward,
 // 16 per channel and row for single tokens, in bf16), and on the way to it the
 // instructions per element (about 14 forward, 38 backward) and the loads in
-// flight.  Measured, bf16, four taps, SiLU: forward 4 x 5120 x 4096, token-major
-// in, channels-first out, 72 us (4.66 TB/s); packed 8192 x 2560 21.9 us (3.9
-// TB/s); backward 8 x 2560 x 2048 80 us (3.1 TB/s, 5 us of it the sum of the
-// runs); single tokens 1024 x 5120 18.0 us (4.7 TB/s).
+// flight.  Measured, bf16, four taps, SiLU, whole calls on inputs that change from
+// call to call: forward 4 x 5120 x 4096, token-major in, channels-first out, 77 us
+// (4.4 TB/s); packed 8192 x 2560 23.6 us (3.6 TB/s); backward 8 x 2560 x 2048 84
+// us (3.0 TB/s, 5 us of it the sum of the runs); single tokens 1024 x 5120 18.5 us
+// (4.5 TB/s).  The figures beside choices below compare kernels on inputs that
+// stay, and are up to a tenth lower.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -31,10 +31,11 @@
 // for about 105 (a packed FMA of three different register pairs issues every
 // third cycle, a packed multiply every second, both measured; scalar FMAs in
 // their place were 2 % (outputs) to 20 % (updates) slower).  Measured, bf16
-// with gate: 131072 x 2048 in one prompt, A[n] = (n+1) A[0], 1.84 ms (pass 1
-// about 0.75, output pass 1.1 = 157 cycles); 16384 x 2048 in 32 prompts of
+// with gate: 131072 x 2048 in one prompt, A[n] = (n+1) A[0], 1.86 ms (pass 1
+// 0.74, fold 0.05, output pass 1.1 = 157 cycles); 16384 x 2048 in 32 prompts of
 // log-normal lengths, general A, 0.36 ms (0.37 where first segments are scanned
-// twice too).
+// twice too).  A unit costs its block some 7 us however short it is: 1024 single
+// tokens of 2560 channels 0.5 ms (the decode step through slots 0.07).
 // Tried and dropped: two of eight pairs of exponentials as polynomials on the
 // FMA pipe (10 to 13 instructions per pair instead of 2: issue-bound, 441
 // against 408 us), two lanes per channel (414 against 393 us), one channel per
@@ -675,7 +676,7 @@ static __global__ void __launch_bounds__(256) scan_packed_fold_kernel(const __gr
     const int64_t hop = int64_t(p.dim) * kDiagN;
     float h = ag[0];
     // eight segments' numbers at a time: one after the other, each would cost a
-    // trip to memory (37 segments of 2048 channels: 82 us, now 14; 293: 43)
+    // trip to memory (37 segments of 2048 channels: 82 us, now 14; 293: 49)
     constexpr int AHEAD = 8;
     for (int k0 = 1; k0 < nseg - 1; k0 += AHEAD) {
         float E[AHEAD], S[AHEAD];
