@@ -171,7 +171,8 @@ struct PackedPlan {
 
 // Lanes per channel and tokens per segment of packed prompts, from the numbers
 // of rows, sequences and channels (the lengths are on the device).  All figures
-// bf16 with gate, general A where none is named, us.
+// bf16 with gate, general A where none is named, us, both sides measured when the
+// rule was chosen (the kernels have become up to 2 % slower since, all alike).
 // Lanes: eight up to 2^20 elements, where the longest sequence's own time counts
 // (257 x 64 fp32 in five prompts 18, four lanes 27; 300 x 768 in one 19 against
 // 24; but 16000 x 256 in 16 78 against 70).  One, which does the least work,
